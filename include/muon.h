@@ -36,7 +36,8 @@
  *  - A handle is bound to the device that was current when it was created
  *    and is not thread-safe.
  *  - Kernels report device-side failures (a bounded wait that expired, a
- *    non-finite norm) through a flag read by muon_last_device_error().
+ *    non-finite norm, a non-finite logit or quantiser input, an index out of
+ *    range) through a flag read by muon_last_device_error().
  */
 #ifndef MUON_GB300_H_
 #define MUON_GB300_H_
@@ -82,7 +83,13 @@ typedef enum {
   MUON_KERNEL_SCALE = 6,          /* ns_steps == 0: O = X / s */
   MUON_KERNEL_ADAMW = 7,          /* AdamW companion */
   MUON_KERNEL_TRANSPOSE = 8,      /* BF16 transpose (resharded step) */
-  MUON_KERNEL_COUNT = 9
+  MUON_KERNEL_MOE_ROUTE = 9,      /* routing to experts and its backward pass */
+  MUON_KERNEL_MOE_PLAN = 10,      /* grouping of slots by expert */
+  MUON_KERNEL_MOE_COMBINE = 11,   /* weighted sum of expert rows and its backward pass */
+  MUON_KERNEL_FP8_QUANTIZE = 12,  /* FP8 quantisation (rows, blocks, columns) */
+  MUON_KERNEL_FP8_PRODUCT = 13,   /* grouped FP8 product */
+  MUON_KERNEL_FP8_WGRAD = 14,     /* grouped FP8 weight gradient */
+  MUON_KERNEL_COUNT = 15
 } muon_kernel_t;
 
 typedef struct {
@@ -376,7 +383,8 @@ muon_status_t muon_newton_schulz_bf16_static(int32_t m, int32_t n, int32_t count
                                              void* stream);
 
 /* Synchronise `stream`, then read and clear the handle's device error
- * flag: MUON_OK, MUON_ERR_TIMEOUT or MUON_ERR_NONFINITE. */
+ * flag: MUON_OK, MUON_ERR_TIMEOUT, MUON_ERR_INVALID_ARG (an index read on
+ * the device was out of range) or MUON_ERR_NONFINITE. */
 muon_status_t muon_last_device_error(muon_handle_t handle, void* stream);
 
 /* AdamW options (decoupled weight decay, bias correction; step >= 1 is the
@@ -402,6 +410,158 @@ muon_status_t muon_adamw_step(muon_handle_t handle, int32_t n_tensors, const int
                               float* const* params_dev, const float* const* grads_dev,
                               float* const* exp_avg_dev, float* const* exp_avg_sq_dev,
                               const muon_adamw_options_t* opts, void* stream);
+
+/* ------------------------------------------------------------------
+ * The mixture-of-experts layer whose weights the step updates: routing of
+ * tokens to experts, grouping of the routed tokens, FP8 products with the
+ * experts' weights, and all of it backwards down to FP32 weight gradients
+ * in the layout muon_step takes ("Frontier Pre-training at Microsoft AI":
+ * 512 routed experts per layer, top-7 routing, MXFP8 training).
+ *
+ * Of T tokens with k experts each, slot i = t k + j is token t's j-th
+ * choice.  muon_moe_plan orders the slots by expert; the r-th of them is
+ * row r, and rows [offsets[e], offsets[e+1]) belong to expert e.  Row
+ * buffers are as long as there are slots (T k rows); the rows past
+ * offsets[experts] (slots without an expert) are neither read nor written.
+ * Nothing is copied to the host: the kernels read offsets on the device.
+ *
+ * FP8 values are e4m3 with one E8M0 scale (the power of two 2^(byte - 127))
+ * per 128 values along the summed dimension.  Hidden sizes are multiples of
+ * 16 (a last block of fewer than 128 values is allowed); device buffers are
+ * 16-byte aligned; inputs and outputs of a call must not overlap.
+ *
+ * A NaN or an infinity that a router or a quantiser meets sets the device
+ * error flag (MUON_ERR_NONFINITE; a logit of -inf is an ordinary mask), an
+ * id, row or offset out of range sets it too (MUON_ERR_INVALID_ARG) and is
+ * left out: no buffer is read or written outside its bounds.
+ * ------------------------------------------------------------------ */
+
+typedef enum { MUON_FP32 = 0, MUON_BF16 = 1 } muon_dtype_t;
+typedef enum { MUON_SCORE_SIGMOID = 0, MUON_SCORE_SOFTMAX = 1 } muon_score_t;
+
+/* Options of the routing. */
+typedef struct {
+  int32_t score;         /* muon_score_t */
+  int32_t groups;        /* experts are split into this many equal groups (1..32) */
+  int32_t top_groups;    /* only the best of them are chosen from (1..groups) */
+  int32_t group_top;     /* a group's value: the sum of its best 1 or 2 choice values */
+  int32_t renormalize;   /* divide a token's weights by their sum */
+  float scale;           /* then multiply by this */
+} muon_route_options_t;
+
+/* Routing of tokens to experts.  With x a token's logits, s_e = sigmoid(x_e)
+ * or softmax(x)_e and c_e = s_e + bias_e:
+ *   ids[t][j]      the experts of the top_k largest c, largest first, equal
+ *                  ones in order of expert, from the top_groups best groups
+ *   weights[t][j]  scale s_e, or scale s_e / (sum of the chosen s)
+ * A softmax without bias and with group_top 1 chooses by x itself.  The
+ * bias takes part in the choice alone.  An expert whose logit is -inf is
+ * closed to the token (so is a NaN or +inf, which is also reported); when
+ * fewer than top_k are open, or mask[t] is 0, the slots left over hold id
+ * -1 and weight 0.  When every chosen score underflows to zero the
+ * renormalised weights are zero.
+ * logits: [tokens][experts] of logits_type; bias: [experts] FP32 or NULL;
+ * mask: [tokens] bytes or NULL; ids: [tokens][top_k] int32; weights:
+ * [tokens][top_k] FP32.  experts 1..1024, top_k 1..min(32, experts).
+ * Errors: INVALID_ARG (sizes, groups not dividing experts, fewer than top_k
+ * experts in top_groups groups, scale not finite), CUDA. */
+muon_status_t muon_moe_route(muon_handle_t handle, int64_t tokens, int32_t experts, int32_t top_k,
+                             const void* logits, int32_t logits_type, const float* bias,
+                             const uint8_t* mask, const muon_route_options_t* opts, int32_t* ids,
+                             float* weights, void* stream);
+
+/* Its backward pass: the gradient of the logits (their type) from that of
+ * the weights (grad_weights: [tokens][top_k] FP32), the choice held fixed.
+ * Every element of grad_logits is written; slots of -1 contribute nothing.
+ * ids as muon_moe_route gave them (distinct experts per token).  Only
+ * score, renormalize and scale of opts matter. */
+muon_status_t muon_moe_route_backward(muon_handle_t handle, int64_t tokens, int32_t experts,
+                                      int32_t top_k, const void* logits, int32_t logits_type,
+                                      const int32_t* ids, const float* grad_weights,
+                                      const muon_route_options_t* opts, void* grad_logits,
+                                      void* stream);
+
+/* Grouping of slots by expert (a stable counting sort).  ids: [n_slots],
+ * -1 for none.  offsets: [experts + 1]; slots: [n_slots], the slot of each
+ * row, -1 past offsets[experts]; pos: [n_slots], the row of each slot or
+ * -1.  Uses the handle's workspace when there are more than 4096 slots:
+ * calls on several streams that use it (also muon_step's) are ordered by
+ * the caller.  Errors: INVALID_ARG, NOMEM, CUDA. */
+muon_status_t muon_moe_plan(muon_handle_t handle, int64_t n_slots, int32_t experts,
+                            const int32_t* ids, int32_t* offsets, int32_t* slots, int32_t* pos,
+                            void* stream);
+
+/* out[t] = sum over j of weights[t][j] y[pos[t][j]] (slots of -1 left out;
+ * weights NULL: ones, the backward pass of sending a token to its rows).
+ * y: [rows][hidden] BF16; out: [tokens][hidden] BF16, summed in FP32 in the
+ * order of j and rounded once. */
+muon_status_t muon_moe_combine(muon_handle_t handle, int64_t tokens, int32_t top_k, int64_t rows,
+                               int32_t hidden, const uint16_t* y, const int32_t* pos,
+                               const float* weights, uint16_t* out, void* stream);
+
+/* Its backward pass: grad_y[pos[t][j]] = weights[t][j] grad_out[t] and
+ * grad_weights[t][j] = <grad_out[t], y[pos[t][j]]> (0 for a slot of -1).
+ * grad_weights NULL: not wanted (y may then be NULL). */
+muon_status_t muon_moe_combine_backward(muon_handle_t handle, int64_t tokens, int32_t top_k,
+                                        int64_t rows, int32_t hidden, const uint16_t* grad_out,
+                                        const uint16_t* y, const int32_t* pos,
+                                        const float* weights, uint16_t* grad_y,
+                                        float* grad_weights, void* stream);
+
+/* FP8 quantisation.  Of a block of 128 values with largest magnitude m the
+ * scale is the least power of two with m / scale <= 448 (1 for zeros), and
+ * q = e4m3(x / scale) to nearest even; NaN stays NaN, infinities saturate.
+ *
+ * Rows: blocks run along a row of x [tokens][hidden] (BF16).  pos NULL: q
+ * [tokens][hidden], scales [tokens][ceil(hidden / 128)].  Otherwise row t is
+ * written to the rows pos[t][j] >= 0 of q and scales (`rows` of them). */
+muon_status_t muon_fp8_quantize_rows(muon_handle_t handle, int64_t tokens, int32_t hidden,
+                                     const uint16_t* x, const int32_t* pos, int32_t top_k,
+                                     int64_t rows, uint8_t* q, uint8_t* scales, void* stream);
+
+/* Weights w [experts][n][k] (w_type), one scale per 128 x 128 block: q
+ * [experts][n][k] with scales [experts][ceil(n / 128)][ceil(k / 128)], and
+ * the transpose qt [experts][k][n] with scales_t transposed alike.  Either
+ * pair may be NULL. */
+muon_status_t muon_fp8_quantize_blocks(muon_handle_t handle, int32_t experts, int32_t n, int32_t k,
+                                       const void* w, int32_t w_type, uint8_t* q, uint8_t* scales,
+                                       uint8_t* qt, uint8_t* scales_t, void* stream);
+
+/* Columns of each expert's rows, for the weight gradient, whose sums run
+ * over rows: blocks of 128 rows of one expert (the last filled with zeros),
+ * written transposed.  An expert's columns of qt [hidden][capacity] start at
+ * 128 times the sum of ceil(rows / 128) over the experts before it; scales:
+ * [capacity / 128][hidden].  capacity is a multiple of 128; rows + 127
+ * experts, rounded down to one, always suffices.  Columns past the last
+ * expert's are not written.  Row r is x[r] of x [x_rows][hidden] (BF16), or
+ * x[slots[r] / top_k] with slots [rows] from muon_moe_plan. */
+muon_status_t muon_fp8_quantize_cols(muon_handle_t handle, int64_t x_rows, int32_t hidden,
+                                     const uint16_t* x, int32_t experts, const int32_t* offsets,
+                                     int64_t rows, const int32_t* slots, int32_t top_k, uint8_t* qt,
+                                     int64_t capacity, uint8_t* scales, void* stream);
+
+/* Grouped FP8 product: y[r] = x[r] w[e]^T for the rows r of each expert e,
+ * FP32 accumulation, rounded once to BF16.  x [rows][k] and x_scales as
+ * muon_fp8_quantize_rows gives them, w [experts][n][k] and w_scales as
+ * muon_fp8_quantize_blocks does; y [rows][n].  The forward pass takes w, the
+ * gradient of its input the transposed weights.  One expert over all rows
+ * is a dense product.  k and n multiples of 16. */
+muon_status_t muon_fp8_grouped_matmul(muon_handle_t handle, int64_t rows, int32_t experts,
+                                      int32_t n, int32_t k, const uint8_t* x,
+                                      const uint8_t* x_scales, const uint8_t* w,
+                                      const uint8_t* w_scales, const int32_t* offsets, uint16_t* y,
+                                      void* stream);
+
+/* Grouped FP8 weight gradient: dw[e] = dY[e]^T X[e] over the rows of each
+ * expert, FP32 (with accumulate: added to dw).  yt [n][capacity] and xt
+ * [k][capacity] with their scales as muon_fp8_quantize_cols gives them for
+ * these offsets; dw [experts][n][k], the layout of muon_step's gradients.
+ * An expert without rows gets zeros (or keeps what it has). */
+muon_status_t muon_fp8_grouped_wgrad(muon_handle_t handle, int32_t experts, int32_t n, int32_t k,
+                                     int64_t capacity, const uint8_t* yt, const uint8_t* yt_scales,
+                                     const uint8_t* xt, const uint8_t* xt_scales,
+                                     const int32_t* offsets, float* dw, int32_t accumulate,
+                                     void* stream);
 
 /* Failure-path self-test of the bounded device waits: launches one small
  * kernel that waits, through the same wait routine the Newton-Schulz

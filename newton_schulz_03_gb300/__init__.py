@@ -15,6 +15,10 @@ from ._native import (  # noqa: F401
     muon_plan_describe, muon_shard_apply, muon_shard_momentum_cast, muon_transpose_bf16, muon_selftest_bounded_wait,
     muon_reset_kernel_stats, muon_set_kernel_timing, muon_status_string, muon_step,
     muon_step_ex, muon_step_host, muon_version, SCALE_NONE, SCALE_SQRT_ASPECT, SCALE_RMS_MATCH,
+    SCORE_SIGMOID, SCORE_SOFTMAX, muon_fp8_cols_capacity, muon_fp8_grouped_matmul,
+    muon_fp8_grouped_wgrad, muon_fp8_quantize_blocks, muon_fp8_quantize_cols,
+    muon_fp8_quantize_rows, muon_moe_combine, muon_moe_combine_backward, muon_moe_plan,
+    muon_moe_route, muon_moe_route_backward,
 )
 
 __all__ = [
@@ -30,4 +34,8 @@ __all__ = [
     "muon_set_kernel_timing", "muon_status_string", "muon_step", "muon_step_ex", "muon_step_host",
     "SCALE_NONE", "SCALE_SQRT_ASPECT", "SCALE_RMS_MATCH",
     "muon_version",
+    "SCORE_SIGMOID", "SCORE_SOFTMAX", "muon_moe_route", "muon_moe_route_backward",
+    "muon_moe_plan", "muon_moe_combine", "muon_moe_combine_backward", "muon_fp8_quantize_rows",
+    "muon_fp8_quantize_blocks", "muon_fp8_quantize_cols", "muon_fp8_cols_capacity",
+    "muon_fp8_grouped_matmul", "muon_fp8_grouped_wgrad",
 ]

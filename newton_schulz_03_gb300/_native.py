@@ -22,7 +22,8 @@ STATUS_NAMES = {
     7: "MUON_ERR_NO_DEVICE",
 }
 KERNEL_NAMES = ("momentum_cast", "norm", "ns_gram", "ns_poly", "ns_update", "apply", "scale",
-                "adamw", "transpose")
+                "adamw", "transpose", "moe_route", "moe_plan", "moe_combine", "fp8_quantize",
+                "fp8_product", "fp8_wgrad")
 N_KERNELS = len(KERNEL_NAMES)
 
 # Symbols the header declares (checked by the CPU test-suite).
@@ -34,7 +35,11 @@ EXPORTED = (
     "muon_newton_schulz_bf16_static", "muon_selftest_bounded_wait", "muon_step_ex",
     "muon_adamw_step", "muon_partition", "muon_host_alloc", "muon_host_free",
     "muon_shard_momentum_cast", "muon_norm_from_sumsq", "muon_transpose_bf16", "muon_shard_apply",
+    "muon_moe_route", "muon_moe_route_backward", "muon_moe_plan", "muon_moe_combine",
+    "muon_moe_combine_backward", "muon_fp8_quantize_rows", "muon_fp8_quantize_blocks",
+    "muon_fp8_quantize_cols", "muon_fp8_grouped_matmul", "muon_fp8_grouped_wgrad",
 )
+SCORE_SIGMOID, SCORE_SOFTMAX = 0, 1
 SCALE_NONE, SCALE_SQRT_ASPECT, SCALE_RMS_MATCH = 0, 1, 2
 
 
@@ -68,6 +73,12 @@ class _AdamwOptions(ctypes.Structure):
                 ("eps", ctypes.c_float), ("wd", ctypes.c_float), ("step", ctypes.c_int32)]
 
 
+class _RouteOptions(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 class _PlanInfo(ctypes.Structure):
     _fields_ = [("n_batches", ctypes.c_int32), ("n_chunks", ctypes.c_int32),
                 ("max_chunk_matrices", ctypes.c_int32), ("matrices", ctypes.c_int64),
@@ -89,6 +100,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         raise ImportError(f"{p} is missing: build it with `python -m newton_schulz_03_gb300.build_lib`")
     lib = ctypes.CDLL(p)
     c_int, c_i32, c_f, c_vp, c_sz = ctypes.c_int, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+    c_i64 = ctypes.c_int64
     P = ctypes.POINTER
     sig = {
         "muon_status_string": (ctypes.c_char_p, [c_int]),
@@ -125,6 +137,25 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "muon_selftest_bounded_wait": (c_int, [c_vp, c_i32, c_vp]),
         "muon_adamw_step": (c_int, [c_vp, c_i32, P(ctypes.c_int64), P(c_vp), P(c_vp), P(c_vp),
                                     P(c_vp), P(_AdamwOptions), c_vp]),
+        "muon_moe_route": (c_int, [c_vp, c_i64, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp,
+                                   P(_RouteOptions), c_vp, c_vp, c_vp]),
+        "muon_moe_route_backward": (c_int, [c_vp, c_i64, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp,
+                                            P(_RouteOptions), c_vp, c_vp]),
+        "muon_moe_plan": (c_int, [c_vp, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
+        "muon_moe_combine": (c_int, [c_vp, c_i64, c_i32, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp,
+                                     c_vp]),
+        "muon_moe_combine_backward": (c_int, [c_vp, c_i64, c_i32, c_i64, c_i32, c_vp, c_vp, c_vp,
+                                              c_vp, c_vp, c_vp, c_vp]),
+        "muon_fp8_quantize_rows": (c_int, [c_vp, c_i64, c_i32, c_vp, c_vp, c_i32, c_i64, c_vp,
+                                           c_vp, c_vp]),
+        "muon_fp8_quantize_blocks": (c_int, [c_vp, c_i32, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp,
+                                             c_vp, c_vp, c_vp]),
+        "muon_fp8_quantize_cols": (c_int, [c_vp, c_i64, c_i32, c_vp, c_i32, c_vp, c_i64, c_vp,
+                                           c_i32, c_vp, c_i64, c_vp, c_vp]),
+        "muon_fp8_grouped_matmul": (c_int, [c_vp, c_i64, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp,
+                                            c_vp, c_vp, c_vp, c_vp]),
+        "muon_fp8_grouped_wgrad": (c_int, [c_vp, c_i32, c_i32, c_i32, c_i64, c_vp, c_vp, c_vp,
+                                           c_vp, c_vp, c_vp, c_i32, c_vp]),
         "muon_set_kernel_timing": (c_int, [c_vp, c_i32]),
         "muon_kernel_stats": (c_int, [c_vp, P(_Stats)]),
         "muon_reset_kernel_stats": (c_int, [c_vp]),
@@ -380,6 +411,182 @@ def muon_adamw_step(handle: int, params: Sequence, grads: Sequence, exp_avg: Seq
     _check(load_library().muon_adamw_step(handle, n, numel, _ptr_array(params), _ptr_array(grads),
                                           _ptr_array(exp_avg), _ptr_array(exp_avg_sq),
                                           ctypes.byref(opts), _stream(stream)))
+
+
+# ------------------------------------------------ mixture-of-experts layer
+_DTYPES = {"torch.float32": 0, "torch.bfloat16": 1}
+
+
+def _dtype(t) -> int:
+    """muon_dtype_t of a tensor."""
+    d = _DTYPES.get(str(t.dtype))
+    if d is None:
+        raise ValueError(f"expected an FP32 or BF16 tensor, got {t.dtype}")
+    return d
+
+
+def _want(name: str, t, shape, dtypes) -> int:
+    """Address of a contiguous CUDA tensor of this shape and type."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if str(t.dtype).removeprefix("torch.") not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(dtypes)}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return _ptr(t)
+
+
+_F32, _BF16, _I32 = ("float32",), ("bfloat16",), ("int32",)
+_F8 = ("float8_e4m3fn", "uint8")
+_E8 = ("uint8", "float8_e8m0fnu")
+_BYTES = ("uint8", "bool")
+
+
+def _nb(n: int) -> int:
+    return -(-n // 128)
+
+
+def muon_moe_route(handle: int, logits, ids, weights, score: int = SCORE_SIGMOID, bias=None,
+                   mask=None, groups: int = 1, top_groups: int = 1, group_top: int = 1,
+                   renormalize: bool = True, scale: float = 1.0, stream=None) -> None:
+    """Experts ``ids`` [tokens, k] (int32) and their ``weights`` (FP32) from
+    the router's ``logits`` [tokens, experts] (FP32 or BF16); ``bias``
+    [experts] takes part in the choice alone, ``mask`` [tokens] switches
+    tokens off."""
+    t, e = logits.shape
+    k = ids.shape[-1]
+    opts = _RouteOptions(score, groups, top_groups, group_top, 1 if renormalize else 0, scale)
+    _check(load_library().muon_moe_route(
+        handle, t, e, k, _want("logits", logits, (t, e), _F32 + _BF16), _dtype(logits),
+        0 if bias is None else _want("bias", bias, (e,), _F32),
+        0 if mask is None else _want("mask", mask, (t,), _BYTES), ctypes.byref(opts),
+        _want("ids", ids, (t, k), _I32), _want("weights", weights, (t, k), _F32),
+        _stream(stream)))
+
+
+def muon_moe_route_backward(handle: int, logits, ids, grad_weights, grad_logits,
+                            score: int = SCORE_SIGMOID, renormalize: bool = True,
+                            scale: float = 1.0, stream=None) -> None:
+    """Gradient of the logits (written whole, the logits' type)."""
+    t, e = logits.shape
+    k = ids.shape[-1]
+    opts = _RouteOptions(score, 1, 1, 1, 1 if renormalize else 0, scale)
+    _check(load_library().muon_moe_route_backward(
+        handle, t, e, k, _want("logits", logits, (t, e), _F32 + _BF16), _dtype(logits),
+        _want("ids", ids, (t, k), _I32), _want("grad_weights", grad_weights, (t, k), _F32),
+        ctypes.byref(opts),
+        _want("grad_logits", grad_logits, (t, e), (str(logits.dtype).removeprefix("torch."),)),
+        _stream(stream)))
+
+
+def muon_moe_plan(handle: int, ids, offsets, slots, pos, stream=None) -> None:
+    """Rows of the slots in order of expert: ``offsets`` [experts + 1],
+    ``slots`` [rows] (the slot of each row), ``pos`` (the row of each slot,
+    the shape of ``ids``); all int32."""
+    n = ids.numel()
+    e = offsets.shape[0] - 1
+    _check(load_library().muon_moe_plan(
+        handle, n, e, _want("ids", ids, ids.shape, _I32), _want("offsets", offsets, (e + 1,), _I32),
+        _want("slots", slots, (n,), _I32), _want("pos", pos, ids.shape, _I32), _stream(stream)))
+
+
+def muon_moe_combine(handle: int, y, pos, weights, out, stream=None) -> None:
+    """out[t] = sum over j of weights[t, j] y[pos[t, j]]; weights None: ones."""
+    (r, d), (t, k) = y.shape, pos.shape
+    _check(load_library().muon_moe_combine(
+        handle, t, k, r, d, _want("y", y, (r, d), _BF16), _want("pos", pos, (t, k), _I32),
+        0 if weights is None else _want("weights", weights, (t, k), _F32),
+        _want("out", out, (t, d), _BF16), _stream(stream)))
+
+
+def muon_moe_combine_backward(handle: int, grad_out, y, pos, weights, grad_y, grad_weights=None,
+                              stream=None) -> None:
+    """Gradients of muon_moe_combine; with ``grad_weights`` None, ``y`` may
+    be None too."""
+    (r, d), (t, k) = grad_y.shape, pos.shape
+    _check(load_library().muon_moe_combine_backward(
+        handle, t, k, r, d, _want("grad_out", grad_out, (t, d), _BF16),
+        0 if y is None else _want("y", y, (r, d), _BF16), _want("pos", pos, (t, k), _I32),
+        0 if weights is None else _want("weights", weights, (t, k), _F32),
+        _want("grad_y", grad_y, (r, d), _BF16),
+        0 if grad_weights is None else _want("grad_weights", grad_weights, (t, k), _F32),
+        _stream(stream)))
+
+
+def muon_fp8_quantize_rows(handle: int, x, q, scales, pos=None, stream=None) -> None:
+    """Rows of ``x`` [tokens, hidden] (BF16) to e4m3 ``q`` with a scale byte
+    (E8M0) per 128; with ``pos`` [tokens, k], row t goes to rows pos[t]."""
+    (t, d), r = x.shape, q.shape[0]
+    k = 0
+    if pos is not None:
+        k = pos.shape[-1]
+    elif r != t:
+        raise ValueError(f"q must have {t} rows, got {r}")
+    _check(load_library().muon_fp8_quantize_rows(
+        handle, t, d, _want("x", x, (t, d), _BF16),
+        0 if pos is None else _want("pos", pos, (t, k), _I32), k, r, _want("q", q, (r, d), _F8),
+        _want("scales", scales, (r, _nb(d)), _E8), _stream(stream)))
+
+
+def muon_fp8_quantize_blocks(handle: int, w, q=None, scales=None, qt=None, scales_t=None,
+                             stream=None) -> None:
+    """Weights ``w`` [experts, n, k] (FP32 or BF16) to e4m3 with a scale byte
+    per 128 x 128 block, as they are (``q``, ``scales``) and transposed
+    (``qt``, ``scales_t``)."""
+    e, n, k = w.shape
+    _check(load_library().muon_fp8_quantize_blocks(
+        handle, e, n, k, _want("w", w, (e, n, k), _F32 + _BF16), _dtype(w),
+        0 if q is None else _want("q", q, (e, n, k), _F8),
+        0 if scales is None else _want("scales", scales, (e, _nb(n), _nb(k)), _E8),
+        0 if qt is None else _want("qt", qt, (e, k, n), _F8),
+        0 if scales_t is None else _want("scales_t", scales_t, (e, _nb(k), _nb(n)), _E8),
+        _stream(stream)))
+
+
+def muon_fp8_cols_capacity(rows: int, experts: int) -> int:
+    """Columns that hold ``rows`` rows of ``experts`` experts, each expert's
+    rounded up to a multiple of 128, however they fall."""
+    return (rows + 127 * min(experts, rows)) // 128 * 128
+
+
+def muon_fp8_quantize_cols(handle: int, x, offsets, qt, scales, slots=None, top_k: int = 1,
+                           stream=None) -> None:
+    """Each expert's rows of ``x`` (or, with ``slots``, of the tokens they
+    come from) in blocks of 128 rows, transposed: ``qt`` [hidden, capacity],
+    ``scales`` [capacity / 128, hidden]."""
+    (xr, d), e, cap = x.shape, offsets.shape[0] - 1, qt.shape[1]
+    rows = xr if slots is None else slots.shape[0]
+    _check(load_library().muon_fp8_quantize_cols(
+        handle, xr, d, _want("x", x, (xr, d), _BF16), e, _want("offsets", offsets, (e + 1,), _I32),
+        rows, 0 if slots is None else _want("slots", slots, (rows,), _I32), top_k,
+        _want("qt", qt, (d, cap), _F8), cap, _want("scales", scales, (cap // 128, d), _E8),
+        _stream(stream)))
+
+
+def muon_fp8_grouped_matmul(handle: int, x, x_scales, w, w_scales, offsets, y,
+                            stream=None) -> None:
+    """y[r] = x[r] w[e]^T for the rows [offsets[e], offsets[e + 1]) of each
+    expert; ``x`` [rows, k], ``w`` [experts, n, k] e4m3, ``y`` [rows, n] BF16."""
+    (r, k), (e, n, _) = x.shape, w.shape
+    _check(load_library().muon_fp8_grouped_matmul(
+        handle, r, e, n, k, _want("x", x, (r, k), _F8),
+        _want("x_scales", x_scales, (r, _nb(k)), _E8), _want("w", w, (e, n, k), _F8),
+        _want("w_scales", w_scales, (e, _nb(n), _nb(k)), _E8),
+        _want("offsets", offsets, (e + 1,), _I32), _want("y", y, (r, n), _BF16), _stream(stream)))
+
+
+def muon_fp8_grouped_wgrad(handle: int, yt, yt_scales, xt, xt_scales, offsets, dw,
+                           accumulate: bool = False, stream=None) -> None:
+    """dw[e] (+)= dY[e]^T X[e] over each expert's rows; ``yt`` [n, capacity],
+    ``xt`` [k, capacity] from muon_fp8_quantize_cols, ``dw`` [experts, n, k]
+    FP32."""
+    (n, cap), k, e = yt.shape, xt.shape[0], offsets.shape[0] - 1
+    _check(load_library().muon_fp8_grouped_wgrad(
+        handle, e, n, k, cap, _want("yt", yt, (n, cap), _F8),
+        _want("yt_scales", yt_scales, (cap // 128, n), _E8), _want("xt", xt, (k, cap), _F8),
+        _want("xt_scales", xt_scales, (cap // 128, k), _E8),
+        _want("offsets", offsets, (e + 1,), _I32), _want("dw", dw, (e, n, k), _F32),
+        1 if accumulate else 0, _stream(stream)))
 
 
 def muon_selftest_bounded_wait(handle: int, limit_ms: int = 50, stream=None) -> None:

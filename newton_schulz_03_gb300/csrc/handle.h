@@ -1,0 +1,41 @@
+// handle.h -- what the host files beside muon_api.cpp see of a handle.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+
+struct muon_handle_s;
+
+namespace muon {
+
+struct HandleInfo {
+  int num_sms;
+  int* dev_err;   // device error word (kDevErr* bits)
+};
+
+// Status of the handle (MUON_OK, or MUON_ERR_INVALID_ARG with its message);
+// makes the handle's device current.
+int handle_info(muon_handle_s* h, HandleInfo* out);
+
+// The handle's workspace, grown to at least `bytes` (a growth synchronises
+// the device).
+int handle_workspace(muon_handle_s* h, size_t bytes, void** out);
+
+// Counts one kernel launch of class `kind` and, with timing on, brackets it
+// with events.
+class LaunchMark {
+ public:
+  LaunchMark(muon_handle_s* h, int kind, cudaStream_t s);
+  ~LaunchMark();
+  LaunchMark(const LaunchMark&) = delete;
+  LaunchMark& operator=(const LaunchMark&) = delete;
+
+ private:
+  muon_handle_s* h_;
+  int kind_;
+  cudaStream_t s_;
+  cudaEvent_t a_;
+};
+
+}  // namespace muon

@@ -1,0 +1,640 @@
+// k_fp8_gemm.cu -- the experts' products on FP8 operands with a power-of-two
+// scale per 128 values, on CTA pairs (tcgen05 cta_group::2, block-scaled MMA).
+//
+//   rows   y[r] = sum_b 2^(sx[r,b] + sw[e,n/128,b]) sum_{k in block b} x[r,k] w[e,n,k]
+//          for the rows r of expert e (forward; with the transposed weights the
+//          gradient of the input)
+//   wgrad  dw[e] = sum over the expert's blocks of 128 rows of dY^T X, each
+//          operand scaled per (128 rows, column)
+//
+// Both have the weights' output rows on the accumulator's lanes (256 per pair
+// tile, 128 per CTA) and, on its columns, an expert's tokens (rows) or the
+// weights' input columns (wgrad).  Tokens are the ragged side: an MMA may have
+// any multiple of 32 columns, so an expert's tokens are cut into
+// ceil(M / 224) tiles of equal width instead of being padded to 128.  224 is
+// the widest that leaves room in TMEM for the scales beside two accumulators
+// (2 x 224 + 32 <= 512 columns).
+//
+// The tensor cores multiply by the scales: each 128-wide K block is four MMAs
+// (K = 32) that read one scale byte per row of A and of B from TMEM.  Scales
+// travel as bytes: two warps per CTA gather the block's 128 + up to 256 bytes,
+// spread them to the 32-bit cells TMEM wants in shared memory, and the MMA
+// thread copies them over (tcgen05.cp) ahead of the block's MMAs.  Every
+// K block has its own cells, so no alignment of the rows is needed.
+//
+// A persistent pair walks the tiles.  Warp 0: TMA producer.  Warp 1: TMEM and,
+// in the even CTA, the MMAs.  Warps 2-5: epilogue, overlapped with the next
+// tile through the second accumulator.  Warps 6-7: scales.  The experts' rows
+// are read from `offsets` on the device: every block sums the experts' tile
+// counts before its first tile, so a call needs no host copy of the routing.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kernels.h"
+#include "launch.cuh"
+#include "moe.h"
+#include "sm103_ptx.cuh"
+
+namespace muon {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kEpiWarps = 4;
+constexpr int kTileM = 256;                       // pair tile: output rows of w / dw
+constexpr int kHalfM = 128;
+constexpr int kBK = 128;                          // K block: one 128-byte swizzle row, one scale
+constexpr int kABytes = kHalfM * kBK;             // 16 KB per CTA and stage
+constexpr int kStages = 6;
+constexpr int kScaleBytes = 512 + 1024;           // per stage: 128 A cells, 256 B cells
+constexpr int kMaxTokens = 224;                   // rows: widest token tile
+constexpr int kWidthUnit = 32;                    // MMA columns come in multiples of this
+constexpr int kGradN = 192;                       // wgrad: columns per tile (a multiple of 32)
+constexpr int kTokenGroup = 8;                    // rows: token tiles that share a sweep over w
+constexpr int kTmemCols = 512;
+constexpr int kTmemScales = 480;
+constexpr int kMaps = kMaxTokens / kWidthUnit;    // B boxes: half a width each
+
+template <bool GRAD>
+struct Layout {
+  static constexpr int kAccCols = GRAD ? kGradN : kMaxTokens;
+  static constexpr int kBBytes = (kAccCols / 2) * kBK;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kOutBuf = GRAD ? 4096 : 2048;          // one 32 x 32 chunk
+  static constexpr int kScaleAt = kStages * kStageBytes;
+  static constexpr int kOutAt = kScaleAt + kStages * kScaleBytes;
+  static constexpr int kTableAt = kOutAt + kEpiWarps * 2 * kOutBuf;
+  static constexpr int kTableBytes = (kMoeMaxExperts + 4) * 4;
+  static constexpr int kBarAt = kTableAt + 2 * kTableBytes;
+  static constexpr int kSmem = kBarAt + 256 + 1024;
+  static_assert(kBBytes % 1024 == 0 && kOutAt % 1024 == 0, "swizzle atoms");
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+};
+
+struct Fp8Args {
+  const uint8_t* a_scales;
+  const uint8_t* b_scales;
+  const int32_t* offsets;
+  int32_t experts;
+  int32_t n;            // rows of w / dw
+  int32_t k;            // rows: contraction; wgrad: columns of dw
+  int64_t rows;         // rows: rows of x and y; wgrad: columns of yt and xt
+  int32_t n_blocks, k_blocks;
+  int32_t tiles_m, tiles_n;
+  __nv_bfloat16* y;
+  int32_t accumulate;
+  int* err;
+};
+
+struct Maps {
+  CUtensorMap a;
+  CUtensorMap b[kMaps];
+  CUtensorMap out;
+};
+
+struct Tile {
+  int expert;
+  int n0;               // first output row
+  int c0;               // first token row (rows) or column of dw (wgrad)
+  int cols;             // tokens or columns that exist
+  int width;            // MMA columns (a multiple of kWidthUnit)
+  int kb0, nkb;         // K blocks
+};
+
+// first[e]: token tiles (rows) or row blocks (wgrad) before expert e;
+// start[e]: its first row.
+template <bool GRAD>
+__device__ __forceinline__ bool decode(const Fp8Args& p, const int32_t* first, const int32_t* start,
+                                       int64_t t, Tile& o) {
+  if (GRAD) {
+    const int per = p.tiles_m * p.tiles_n;
+    o.expert = static_cast<int>(t / per);
+    if (o.expert >= p.experts) return false;
+    const int l = static_cast<int>(t - static_cast<int64_t>(o.expert) * per);
+    const int tn = l / p.tiles_m;
+    o.n0 = (l - tn * p.tiles_m) * kTileM;
+    o.c0 = tn * kGradN;
+    o.cols = min(kGradN, p.k - o.c0);
+    o.width = kGradN;
+    o.kb0 = first[o.expert];
+    o.nkb = first[o.expert + 1] - o.kb0;
+    return true;
+  }
+  if (t >= static_cast<int64_t>(first[p.experts]) * p.tiles_m) return false;
+  const int g = static_cast<int>(t / p.tiles_m);
+  int lo = 0, hi = p.experts;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= g) lo = mid; else hi = mid;
+  }
+  // Within an expert: groups of kTokenGroup token tiles sweep over w
+  // together, so that w is read from HBM once per group.
+  const int tiles = first[lo + 1] - first[lo];
+  const int64_t l = t - static_cast<int64_t>(first[lo]) * p.tiles_m;
+  const int group = static_cast<int>(l / (kTokenGroup * p.tiles_m));
+  const int r = static_cast<int>(l - static_cast<int64_t>(group) * kTokenGroup * p.tiles_m);
+  const int in_group = min(kTokenGroup, tiles - group * kTokenGroup);
+  const int tm = r / in_group;
+  const int i = group * kTokenGroup + (r - tm * in_group);
+  const int m = start[lo + 1] - start[lo];
+  o.expert = lo;
+  o.n0 = tm * kTileM;
+  o.width = ((m + tiles - 1) / tiles + kWidthUnit - 1) / kWidthUnit * kWidthUnit;
+  o.c0 = start[lo] + i * o.width;
+  o.cols = min(o.width, m - i * o.width);
+  o.kb0 = 0;
+  o.nkb = p.k_blocks;
+  return true;
+}
+
+// Fills first[] and start[] (256 threads, 4 experts each).
+template <bool GRAD>
+__device__ __forceinline__ void scan_experts(const Fp8Args& p, int32_t* first, int32_t* start,
+                                             int32_t* warp_total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int count[4], sum = 0;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = threadIdx.x * 4 + i;
+    count[i] = 0;
+    if (e < p.experts) {
+      const int a = p.offsets[e], b = p.offsets[e + 1];
+      if (GRAD) {
+        bad = bad || a < 0 || b < a;
+        count[i] = (max(0, b - a) + kBK - 1) / kBK;
+      } else {
+        // Rows outside x and y are never touched, whatever offsets holds.
+        const int top = static_cast<int>(p.rows);
+        const int ca = min(max(a, 0), top), cb = min(max(b, ca), top);
+        bad = bad || ca != a || cb != b;
+        start[e] = ca;
+        if (e == p.experts - 1) start[p.experts] = cb;
+        count[i] = (cb - ca + kMaxTokens - 1) / kMaxTokens;
+      }
+    }
+    sum += count[i];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_total[warp] = incl;
+  __syncthreads();
+  int at = incl - sum;
+  for (int i = 0; i < warp; ++i) at += warp_total[i];
+  const int limit = GRAD ? static_cast<int>(p.rows / kBK) : INT32_MAX;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = threadIdx.x * 4 + i;
+    if (e <= p.experts) {
+      bad = bad || at > limit;
+      first[e] = min(at, limit);
+    }
+    at += count[i];
+  }
+  if (threadIdx.x == kThreads - 1 && p.experts == 4 * kThreads) {
+    bad = bad || at > limit;
+    first[p.experts] = min(at, limit);
+  }
+  if (bad && blockIdx.x == 0) atomicOr(p.err, kDevErrIndex);
+}
+
+template <bool GRAD>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    fp8_product_kernel(const __grid_constant__ Maps maps, const Fp8Args p) {
+  using L = Layout<GRAD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  int32_t* first = reinterpret_cast<int32_t*>(smem + L::kTableAt);
+  int32_t* start = reinterpret_cast<int32_t*>(smem + L::kTableAt + L::kTableBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarAt);
+  uint64_t* empty = full + kStages;
+  uint64_t* tmem_full = empty + kStages;
+  uint64_t* tmem_empty = tmem_full + 2;
+  uint64_t* drain = tmem_empty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int32_t* warp_total = reinterpret_cast<int32_t*>(tmem_holder + 2);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1;
+  const int npairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&full[s], 1 + 2);            // the TMA bytes, both CTAs' scales
+      ptx::mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(&tmem_full[a], 1);
+      ptx::mbar_init(&tmem_empty[a], 2 * kEpiWarps * 32);
+    }
+    ptx::mbar_init(drain, 1);
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::tma_prefetch_desc(&maps.a);
+    if (GRAD) ptx::tma_prefetch_desc(&maps.out);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(tmem_holder, kTmemCols);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  grid_dep_wait();
+  grid_dep_launch();
+  scan_experts<GRAD>(p, first, start, warp_total);
+  __syncthreads();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producers
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;
+      bool ok = true;
+      Tile o;
+      for (int64_t t = pair; ok && decode<GRAD>(p, first, start, t, o); t += npairs) {
+        const int half = o.width / 2;
+        const int box = GRAD ? 0 : o.width / kWidthUnit - 1;
+        const uint32_t b_bytes = static_cast<uint32_t>(half * kBK);
+        const int row_a = o.n0 + static_cast<int>(rank) * kHalfM;
+        const int row_b = o.c0 + static_cast<int>(rank) * half;
+        for (int kb = 0; kb < o.nkb; ++kb) {
+          if (!ptx::mbar_wait_cluster(&empty[stage], phase ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full_leader = ptx::mapa_shared(ptx::smem_addr(&full[stage]), 0);
+          if (leader) ptx::mbar_arrive_expect_tx(&full[stage], 2u * (kABytes + b_bytes));
+          uint8_t* sa = smem + stage * L::kStageBytes;
+          ptx::tma_load_3d_pair(sa, &maps.a, full_leader, (o.kb0 + kb) * kBK, row_a,
+                                GRAD ? 0 : o.expert);
+          ptx::tma_load_3d_pair(sa + kABytes, &maps.b[box], full_leader, (o.kb0 + kb) * kBK, row_b,
+                                0);
+          ++issued;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        atomicOr(p.err, kDevErrTimeout);
+      }
+      const int pending = issued < kStages ? issued : kStages;
+      for (int j = 0; j < pending; ++j) {
+        if (stage == 0) {
+          stage = kStages;
+          phase ^= 1u;
+        }
+        --stage;
+        ptx::mbar_wait_cluster(&empty[stage], phase, nullptr);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (lane == 0 && leader) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      uint32_t cells = 0;
+      bool ok = true;
+      Tile o;
+      for (int64_t t = pair; ok && decode<GRAD>(p, first, start, t, o); t += npairs) {
+        if (o.nkb == 0) continue;
+        if (!ptx::mbar_wait_cluster(&tmem_empty[acc], acc_phase ^ 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * L::kAccCols);
+        const uint32_t idesc = ptx::idesc_mxf8(kTileM, o.width);
+        for (int kb = 0; kb < o.nkb; ++kb) {
+          if (!ptx::mbar_wait_cluster(&full[stage], phase, abort_flag)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          // Two sets of scale cells in turn.
+          const uint32_t sa_tmem = tmem_base + kTmemScales + cells * 16, sb_tmem = sa_tmem + 4;
+          cells ^= 1u;
+          const uint32_t ss = ptx::smem_addr(smem + L::kScaleAt + stage * kScaleBytes);
+          ptx::tc_copy_scales_pair(sa_tmem, ptx::smem_desc_scales(ss));
+          ptx::tc_copy_scales_pair(sb_tmem, ptx::smem_desc_scales(ss + 512));
+          if (o.width > 128) ptx::tc_copy_scales_pair(sb_tmem + 4, ptx::smem_desc_scales(ss + 1024));
+          const uint32_t sa = ptx::smem_addr(smem + stage * L::kStageBytes);
+          const uint32_t sb = sa + kABytes;
+#pragma unroll
+          for (int k = 0; k < kBK / 32; ++k)
+            ptx::tc_mma_mxf8_pair(d_tmem, ptx::smem_desc_sw128(sa + k * 32, 16, 1024),
+                                  ptx::smem_desc_sw128(sb + k * 32, 16, 1024), idesc, sa_tmem,
+                                  sb_tmem, (kb | k) != 0 ? 1u : 0u);
+          ptx::tc_commit_pair_multicast(&empty[stage], 0x3);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        ptx::tc_commit_pair_multicast(&tmem_full[acc], 0x3);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        atomicOr(p.err, kDevErrTimeout);
+      }
+      ptx::tc_commit_pair(drain);
+      ptx::mbar_wait(drain, 0, nullptr);
+    }
+  } else if (warp < 2 + kEpiWarps) {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int quad = warp & 3;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    const uint32_t empty_leader0 = ptx::mapa_shared(ptx::smem_addr(&tmem_empty[0]), 0);
+    const uint32_t empty_leader1 = ptx::mapa_shared(ptx::smem_addr(&tmem_empty[1]), 0);
+    uint8_t* stage_out = smem + L::kOutAt + (warp - 2) * 2 * L::kOutBuf;
+    int issued = 0;
+    Tile o;
+    for (int64_t t = pair; decode<GRAD>(p, first, start, t, o); t += npairs) {
+      const int row0 = o.n0 + static_cast<int>(rank) * kHalfM + quad * 32;
+      const bool empty_sum = o.nkb == 0;
+      if (empty_sum && p.accumulate) continue;
+      if (!empty_sum) {
+        const bool got = ptx::mbar_wait_cluster(&tmem_full[acc], acc_phase, abort_flag);
+        if (!__all_sync(0xffffffffu, got)) {
+          if (lane == 0) {
+            *abort_flag = 1;
+            atomicOr(p.err, kDevErrTimeout);
+          }
+          break;
+        }
+        ptx::tc_fence_after();
+      }
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
+                             static_cast<uint32_t>(acc * L::kAccCols);
+      for (int cb = 0; cb * 32 < o.cols; ++cb) {
+        uint32_t v[32];
+        __syncwarp();
+        if (!empty_sum) {
+          ptx::tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(cb * 32), v);
+          ptx::tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0u;
+        }
+        if (GRAD && row0 >= p.n) continue;
+        uint8_t* buf = stage_out + (issued & 1) * L::kOutBuf;
+        ++issued;
+        if (GRAD) {
+          // 32 rows x 128 bytes, 16-byte chunk q of row r at q ^ (r & 7): the
+          // output map's 128-byte swizzle.  A buffer is free once the store
+          // before the last has read it.
+          if (lane == 0) ptx::bulk_wait_read<1>();
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (p.accumulate)
+              ptx::tma_reduce_add_3d(&maps.out, buf, o.c0 + cb * 32, row0, o.expert);
+            else
+              ptx::tma_store_3d(&maps.out, buf, o.c0 + cb * 32, row0, o.expert);
+            ptx::bulk_commit();
+          }
+        } else {
+          // A lane holds one output column of 32 tokens: turned in shared
+          // memory into 64 bytes per token, rounded once to BF16.
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            *reinterpret_cast<__nv_bfloat16*>(buf + j * 64 + lane * 2) =
+                __float2bfloat16_rn(__uint_as_float(v[j]));
+          __syncwarp();
+          const int n = row0 + (lane & 3) * 8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int tok = i * 8 + (lane >> 2);
+            if (cb * 32 + tok < o.cols && n < p.n)
+              *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(o.c0 + cb * 32 + tok) * p.n + n) =
+                  *reinterpret_cast<const uint4*>(buf + tok * 64 + (lane & 3) * 16);
+          }
+        }
+      }
+      if (!empty_sum) {
+        ptx::tc_fence_before();
+        ptx::mbar_arrive_cluster(acc ? empty_leader1 : empty_leader0);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+    }
+    if (GRAD && lane == 0) ptx::bulk_wait_all();
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ scales (both CTAs)
+    const int which = warp - 2 - kEpiWarps;       // K blocks which, which + 2, ...
+    int stage = 0;
+    uint32_t phase = 0;
+    uint32_t turn = 0;
+    bool ok = true;
+    Tile o;
+    for (int64_t t = pair; ok && decode<GRAD>(p, first, start, t, o); t += npairs) {
+      const int row_a = o.n0 + static_cast<int>(rank) * kHalfM;
+      for (int kb = 0; kb < o.nkb; ++kb) {
+        if (turn == static_cast<uint32_t>(which)) {
+          uint32_t a[4], b[8];
+          const int64_t at = o.kb0 + kb;
+          if (GRAD) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = row_a + i * 32 + lane;
+              a[i] = r < p.n ? __ldg(p.a_scales + at * p.n + r) : 127u;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int c = o.c0 + i * 32 + lane;
+              b[i] = i * 32 < kGradN && c < p.k ? __ldg(p.b_scales + at * p.k + c) : 127u;
+            }
+          } else {
+            const uint32_t w =
+                row_a < p.n ? __ldg(p.a_scales + (static_cast<int64_t>(o.expert) * p.n_blocks +
+                                                  row_a / kBK) * p.k_blocks + at)
+                            : 127u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a[i] = w;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int c = i * 32 + lane;
+              b[i] = c < o.cols ? __ldg(p.b_scales + static_cast<int64_t>(o.c0 + c) * p.k_blocks + at)
+                                : 127u;
+            }
+          }
+          const bool got = ptx::mbar_wait_cluster(&empty[stage], phase ^ 1u, abort_flag);
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
+          }
+          // Lane l's 16 bytes hold the cells of rows l, l + 32, l + 64, l + 96.
+          uint4* cells = reinterpret_cast<uint4*>(smem + L::kScaleAt + stage * kScaleBytes);
+          cells[lane] = make_uint4(a[0], a[1], a[2], a[3]);
+          cells[32 + lane] = make_uint4(b[0], b[1], b[2], b[3]);
+          cells[64 + lane] = make_uint4(b[4], b[5], b[6], b[7]);
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&full[stage]), 0));
+        }
+        turn ^= 1u;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      atomicOr(p.err, kDevErrTimeout);
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// (cols, rows, count) of bytes or FP32 values, 128-byte swizzle, zero fill.
+bool encode(CUtensorMap* map, bool fp32, const void* ptr, int64_t cols, int64_t rows, int64_t count,
+            int box_cols, int box_rows) {
+  EncodeFn enc = reinterpret_cast<EncodeFn>(tensor_map_encoder());
+  if (enc == nullptr) return false;
+  const cuuint64_t el = fp32 ? 4 : 1;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(count)};
+  const cuuint64_t strides[2] = {dims[0] * el, dims[0] * dims[1] * el};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1u};
+  const cuuint32_t step[3] = {1u, 1u, 1u};
+  return enc(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+             const_cast<void*>(ptr), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool GRAD>
+cudaError_t launch(const Maps& maps, const Fp8Args& p, int64_t max_tiles, int num_sms,
+                   cudaStream_t s) {
+  static int resident = 0;                        // pairs that fit the GPU at once
+  if (resident == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Layout<GRAD>::kSmem;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_product_kernel<GRAD>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = 1;
+    }
+    resident = n;
+  }
+  int64_t pairs = resident;
+  if (pairs > num_sms / 2) pairs = num_sms / 2;
+  if (pairs > max_tiles) pairs = max_tiles;
+  if (pairs < 1) pairs = 1;
+  return launch_pdl(fp8_product_kernel<GRAD>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads),
+                    Layout<GRAD>::kSmem, s, maps, p);
+}
+
+}  // namespace
+
+cudaError_t fp8_gemm_init() {
+  cudaError_t e = cudaFuncSetAttribute(fp8_product_kernel<false>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Layout<false>::kSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(fp8_product_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Layout<true>::kSmem);
+  return e;
+}
+
+cudaError_t launch_fp8_grouped_matmul(const uint8_t* x, const uint8_t* x_scales, const uint8_t* w,
+                                      const uint8_t* w_scales, const int32_t* offsets, int experts,
+                                      int64_t rows, int n, int k, uint16_t* y, int* err,
+                                      int num_sms, cudaStream_t s) {
+  Maps maps;
+  bool ok = encode(&maps.a, false, w, k, n, experts, kBK, kHalfM);
+  for (int i = 0; i < kMaps; ++i)
+    ok = ok && encode(&maps.b[i], false, x, k, rows, 1, kBK, (i + 1) * (kWidthUnit / 2));
+  if (!ok) return cudaErrorInvalidValue;
+  maps.out = maps.a;
+  Fp8Args p{};
+  p.a_scales = w_scales;
+  p.b_scales = x_scales;
+  p.offsets = offsets;
+  p.experts = experts;
+  p.n = n;
+  p.k = k;
+  p.rows = rows;
+  p.n_blocks = (n + kBK - 1) / kBK;
+  p.k_blocks = (k + kBK - 1) / kBK;
+  p.tiles_m = (n + kTileM - 1) / kTileM;
+  p.y = reinterpret_cast<__nv_bfloat16*>(y);
+  p.err = err;
+  const int64_t token_tiles = (rows < experts ? rows : experts) + rows / kMaxTokens;
+  return launch<false>(maps, p, token_tiles * p.tiles_m, num_sms, s);
+}
+
+cudaError_t launch_fp8_grouped_wgrad(const uint8_t* yt, const uint8_t* yt_scales,
+                                     const uint8_t* xt, const uint8_t* xt_scales,
+                                     const int32_t* offsets, int experts, int64_t cap, int n, int k,
+                                     float* dw, bool accumulate, int* err, int num_sms,
+                                     cudaStream_t s) {
+  Maps maps;
+  bool ok = encode(&maps.a, false, yt, cap, n, 1, kBK, kHalfM);
+  ok = ok && encode(&maps.b[0], false, xt, cap, k, 1, kBK, kGradN / 2);
+  ok = ok && encode(&maps.out, true, dw, k, n, experts, 32, 32);
+  if (!ok) return cudaErrorInvalidValue;
+  for (int i = 1; i < kMaps; ++i) maps.b[i] = maps.b[0];
+  Fp8Args p{};
+  p.a_scales = yt_scales;
+  p.b_scales = xt_scales;
+  p.offsets = offsets;
+  p.experts = experts;
+  p.n = n;
+  p.k = k;
+  p.rows = cap;
+  p.tiles_m = (n + kTileM - 1) / kTileM;
+  p.tiles_n = (k + kGradN - 1) / kGradN;
+  p.accumulate = accumulate ? 1 : 0;
+  p.err = err;
+  return launch<true>(maps, p, int64_t(experts) * p.tiles_m * p.tiles_n, num_sms, s);
+}
+
+}  // namespace muon

@@ -1,0 +1,388 @@
+// k_fp8_quantize.cu -- FP8 (e4m3) quantisation with one power-of-two scale
+// (E8M0) per block of 128, in the three layouts the grouped products read.
+//
+// Of a block with largest magnitude m: e = the least integer with
+// m / 2^e <= 448 (the largest e4m3 value), q = e4m3(x / 2^e) to nearest even,
+// stored scale byte e + 127 (a block of zeros: 127, i.e. 1).  448 = 1.75 2^8,
+// so with m = f 2^p, f in [1, 2): e = p - 8, plus 1 when f > 1.75 -- read off
+// the FP32 bits, and x / 2^e is an exact multiplication: the only rounding is
+// to e4m3.  The tensor cores apply such scales themselves; FP32 scales would
+// need every partial sum read back and multiplied.
+//   rows    1 x 128 along a row; a token's row can be written to each of its
+//           experts' rows (quantised once, written k times)
+//   blocks  128 x 128 of a weight matrix, as it is and transposed: the same
+//           scale serves the product with W and with its transpose
+//   cols    128 x 1 along the rows of one expert, written transposed: the
+//           operands of the weight gradient, whose sums run over rows
+// A NaN stays NaN, an infinity becomes the largest value; both are reported
+// through the device error word.  Every kernel is bound by HBM: each value is
+// read once and written as one byte.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <cstdint>
+
+#include "kernels.h"
+#include "launch.cuh"
+#include "moe.h"
+
+namespace muon {
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// Exponent e of the scale of a block whose largest magnitude has these FP32
+// bits (an infinity: the largest finite exponent's).
+__device__ __forceinline__ int scale_exponent(uint32_t bits) {
+  if (bits == 0u) return 0;
+  const int p = static_cast<int>(bits >> 23) - 127;
+  if (p == 128) return 120;
+  if (p == -127) return -127;             // subnormal: 2^-127 serves all of them
+  return max(-127, p - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0));
+}
+
+// 2^-e as FP32, -127 <= e <= 120.
+__device__ __forceinline__ float inverse_scale(int e) {
+  return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+}
+
+// Largest magnitude as FP32 bits; NaN payloads do not take part.
+__device__ __forceinline__ uint32_t mag(float v, bool& bad) {
+  const uint32_t u = __float_as_uint(v) & 0x7fffffffu;
+  if (u >= kInfBits) bad = true;
+  return u > kInfBits ? 0u : u;
+}
+
+// Four values times `inv` as e4m3 bytes, saturating.
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d, float inv) {
+  const __nv_fp8x2_storage_t p =
+      __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3);
+  const __nv_fp8x2_storage_t q =
+      __nv_cvt_float2_to_fp8x2(make_float2(c * inv, d * inv), __NV_SATFINITE, __NV_E4M3);
+  return static_cast<uint32_t>(p) | (static_cast<uint32_t>(q) << 16);
+}
+
+__device__ __forceinline__ float lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// ------------------------------------------------------------------ rows
+// Half a warp per block of 128 values: 8 values (16 bytes) per lane.
+constexpr int kRowThreads = 256;
+
+__global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(
+    const uint16_t* __restrict__ x, int64_t tokens, int d, int blocks,
+    const int32_t* __restrict__ pos, int k, int64_t rows, uint8_t* __restrict__ q,
+    uint8_t* __restrict__ scales, int* err) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x) >> 4;
+  const int sub = threadIdx.x & 15;
+  const int64_t t = unit / blocks;
+  const int b = static_cast<int>(unit - t * blocks);
+  const bool live = t < tokens;
+  const int c = b * kFp8Block + sub * 8;
+  const bool in = live && c < d;
+  uint4 u = make_uint4(0, 0, 0, 0);
+  if (in) u = *reinterpret_cast<const uint4*>(x + t * d + c);
+  const float v[8] = {lo(u.x), hi(u.x), lo(u.y), hi(u.y), lo(u.z), hi(u.z), lo(u.w), hi(u.w)};
+  bool bad = false;
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, mag(v[i], bad));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
+  if (bad) atomicOr(err, kDevErrInput);
+  if (!live) return;
+  const int e = scale_exponent(m);
+  const float inv = inverse_scale(e);
+  const uint2 out = make_uint2(to_e4m3x4(v[0], v[1], v[2], v[3], inv),
+                               to_e4m3x4(v[4], v[5], v[6], v[7], inv));
+  if (pos == nullptr) {
+    if (in) *reinterpret_cast<uint2*>(q + t * d + c) = out;
+    if (sub == 0) scales[t * blocks + b] = static_cast<uint8_t>(e + 127);
+    return;
+  }
+  for (int j = 0; j < k; ++j) {
+    const int r = pos[t * k + j];
+    if (r < 0 || r >= rows) {
+      if (r != -1) atomicOr(err, kDevErrIndex);
+      continue;
+    }
+    if (in) *reinterpret_cast<uint2*>(q + static_cast<int64_t>(r) * d + c) = out;
+    if (sub == 0) scales[static_cast<int64_t>(r) * blocks + b] = static_cast<uint8_t>(e + 127);
+  }
+}
+
+// ------------------------------------------------------------------ tiles
+// A 128 x 128 tile per block of 256 threads: warp w holds rows 16 w .. 16 w +
+// 15, lane l columns 4 l .. 4 l + 3.  A thread's 16 rows of one column are 16
+// consecutive bytes of the transposed tile, which is put together in shared
+// memory (16-byte chunks, chunk index XORed with the column's group of four so
+// that both the writes and the reads hit distinct banks) and written as rows
+// of up to 128 bytes.
+constexpr int kTileThreads = 256;
+
+__device__ __forceinline__ uint32_t tile_chunk(int col, int chunk) {
+  return static_cast<uint32_t>(col * 128 + ((chunk ^ ((col >> 2) & 7)) << 4));
+}
+
+// words[r] holds row r's four bytes of this thread; stores its 16 x 4 piece.
+__device__ __forceinline__ void put_transposed(uint8_t* tile, const uint32_t (&words)[16], int warp,
+                                               int lane) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t out[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      // Byte c of four rows: a 4 x 4 byte transpose, one column at a time.
+      const uint32_t ab = __byte_perm(words[4 * g], words[4 * g + 1], 0x0040u + c * 0x0011u);
+      const uint32_t cd = __byte_perm(words[4 * g + 2], words[4 * g + 3], 0x0040u + c * 0x0011u);
+      out[g] = __byte_perm(ab, cd, 0x5410u);
+    }
+    *reinterpret_cast<uint4*>(tile + tile_chunk(lane * 4 + c, warp)) =
+        make_uint4(out[0], out[1], out[2], out[3]);
+  }
+}
+
+// Rows (the source's columns) of the transposed tile to dst, `width` bytes
+// (a multiple of 16) each.
+__device__ __forceinline__ void write_transposed(const uint8_t* tile, uint8_t* dst, int64_t pitch,
+                                                 int cols, int width) {
+#pragma unroll
+  for (int i = 0; i < 128 * 8 / kTileThreads; ++i) {
+    const int at = i * kTileThreads + threadIdx.x;
+    const int col = at >> 3, chunk = at & 7;
+    if (col < cols && chunk * 16 < width)
+      *reinterpret_cast<uint4*>(dst + col * pitch + chunk * 16) =
+          *reinterpret_cast<const uint4*>(tile + tile_chunk(col, chunk));
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float4 load_weights(const void* w, int64_t at) {
+  if (BF16) {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + at);
+    return make_float4(lo(u.x), hi(u.x), lo(u.y), hi(u.y));
+  }
+  return __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(w) + at));
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kTileThreads) quantize_blocks_kernel(
+    const void* __restrict__ w, int n, int k, uint8_t* __restrict__ q,
+    uint8_t* __restrict__ scales, uint8_t* __restrict__ qt, uint8_t* __restrict__ scales_t,
+    int* err) {
+  __shared__ __align__(16) uint8_t tile[128 * 128];
+  __shared__ uint32_t warp_max[kTileThreads / 32];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nb = (n + kFp8Block - 1) / kFp8Block, kb = (k + kFp8Block - 1) / kFp8Block;
+  const int per = nb * kb;
+  const int64_t expert = blockIdx.x / per;
+  const int in_expert = static_cast<int>(blockIdx.x - expert * per);
+  const int bn = in_expert / kb, bk = in_expert - bn * kb;
+  const int n0 = bn * kFp8Block, k0 = bk * kFp8Block;
+  const int row0 = n0 + warp * 16, col = k0 + lane * 4;
+  const int64_t base = expert * n * k;
+
+  float4 v[16];
+  bool bad = false;
+  uint32_t m = 0u;
+#pragma unroll
+  for (int r = 0; r < 16; ++r)
+    v[r] = row0 + r < n && col < k ? load_weights<BF16>(w, base + static_cast<int64_t>(row0 + r) * k + col)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int r = 0; r < 16; ++r)
+    m = max(max(m, max(mag(v[r].x, bad), mag(v[r].y, bad))), max(mag(v[r].z, bad), mag(v[r].w, bad)));
+  m = __reduce_max_sync(kAll, m);
+  if (bad) atomicOr(err, kDevErrInput);
+  if (lane == 0) warp_max[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kTileThreads / 32; ++i) m = max(m, warp_max[i]);
+  const int e = scale_exponent(m);
+  const float inv = inverse_scale(e);
+  uint32_t words[16];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) words[r] = to_e4m3x4(v[r].x, v[r].y, v[r].z, v[r].w, inv);
+  if (q != nullptr) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      if (row0 + r < n && col < k)
+        *reinterpret_cast<uint32_t*>(q + base + static_cast<int64_t>(row0 + r) * k + col) = words[r];
+    if (threadIdx.x == 0) scales[(expert * nb + bn) * kb + bk] = static_cast<uint8_t>(e + 127);
+  }
+  if (qt != nullptr) {
+    put_transposed(tile, words, warp, lane);
+    __syncthreads();
+    write_transposed(tile, qt + base + static_cast<int64_t>(k0) * n + n0, n, min(kFp8Block, k - k0),
+                     min(kFp8Block, n - n0));
+    if (threadIdx.x == 0) scales_t[(expert * kb + bk) * nb + bn] = static_cast<uint8_t>(e + 127);
+  }
+}
+
+// ------------------------------------------------------------------ columns
+// Persistent blocks over (128-column stripe, block of 128 rows of one expert),
+// the row blocks of a stripe one after the other: a stripe of the gathered x
+// (tokens x 256 bytes) is read from HBM once and from L2 for the token's
+// other experts.
+__global__ void __launch_bounds__(kTileThreads) quantize_cols_kernel(
+    const uint16_t* __restrict__ x, int64_t x_rows, int d, const int32_t* __restrict__ offsets,
+    int experts, const int32_t* __restrict__ slots, int top_k, int64_t rows,
+    uint8_t* __restrict__ qt, int64_t cap, uint8_t* __restrict__ scales, int* err) {
+  __shared__ __align__(16) uint8_t tile[128 * 128];
+  __shared__ uint32_t col_max[kTileThreads / 32][128];
+  __shared__ int32_t first[kMoeMaxExperts + 1];   // first row block of each expert
+  __shared__ int32_t warp_total[kTileThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // Row blocks before each expert: an exclusive scan, 4 experts per thread.
+  int count[4], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = threadIdx.x * 4 + i;
+    count[i] = e < experts ? (max(0, offsets[e + 1] - offsets[e]) + 127) / 128 : 0;
+    sum += count[i];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kAll, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_total[warp] = incl;
+  __syncthreads();
+  int at = incl - sum;
+  for (int i = 0; i < warp; ++i) at += warp_total[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = threadIdx.x * 4 + i;
+    if (e <= experts) first[e] = at;
+    at += count[i];
+  }
+  if (threadIdx.x == kTileThreads - 1 && experts == 4 * kTileThreads) first[experts] = at;
+  __syncthreads();
+  int blocks = first[experts];
+  if (blocks > cap / 128) {                       // the caller's buffers are too short
+    if (threadIdx.x == 0) atomicOr(err, kDevErrIndex);
+    blocks = static_cast<int>(cap / 128);
+  }
+  const int stripes = (d + 127) / 128;
+  const int64_t tiles = static_cast<int64_t>(stripes) * blocks;
+
+  for (int64_t tid = blockIdx.x; tid < tiles; tid += gridDim.x) {
+    const int stripe = static_cast<int>(tid / blocks);
+    const int b = static_cast<int>(tid - static_cast<int64_t>(stripe) * blocks);
+    // The expert of row block b: the last one that starts at or before it.
+    int lo_e = 0, hi_e = experts;
+    while (hi_e - lo_e > 1) {
+      const int mid = (lo_e + hi_e) >> 1;
+      if (first[mid] <= b) lo_e = mid; else hi_e = mid;
+    }
+    const int64_t row_end = offsets[lo_e + 1];
+    const int64_t row0 = offsets[lo_e] + static_cast<int64_t>(b - first[lo_e]) * 128 + warp * 16;
+    const int c0 = stripe * 128, col = c0 + lane * 4;
+
+    // Lane r of the warp looks up row r's source once.
+    int64_t src = -1;
+    if (lane < 16 && row0 + lane < row_end) {
+      src = row0 + lane;
+      if (src < 0 || src >= rows) {
+        src = -1;
+      } else if (slots != nullptr) {
+        const int slot = slots[src];
+        src = slot >= 0 ? slot / top_k : -1;
+      }
+      if (src < 0 || src >= x_rows) {
+        atomicOr(err, kDevErrIndex);
+        src = -1;
+      }
+    }
+    uint2 u[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int64_t from = __shfl_sync(kAll, src, r);
+      u[r] = from >= 0 && col < d ? *reinterpret_cast<const uint2*>(x + from * d + col)
+                                  : make_uint2(0u, 0u);
+    }
+    bool bad = false;
+    uint32_t m[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      m[0] = max(m[0], mag(lo(u[r].x), bad));
+      m[1] = max(m[1], mag(hi(u[r].x), bad));
+      m[2] = max(m[2], mag(lo(u[r].y), bad));
+      m[3] = max(m[3], mag(hi(u[r].y), bad));
+    }
+    if (bad) atomicOr(err, kDevErrInput);
+    *reinterpret_cast<uint4*>(&col_max[warp][lane * 4]) = make_uint4(m[0], m[1], m[2], m[3]);
+    __syncthreads();
+    float inv[4];
+    int ex[4];
+#pragma unroll
+    for (int w = 0; w < kTileThreads / 32; ++w) {
+      const uint4 o = *reinterpret_cast<const uint4*>(&col_max[w][lane * 4]);
+      m[0] = max(m[0], o.x); m[1] = max(m[1], o.y); m[2] = max(m[2], o.z); m[3] = max(m[3], o.w);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      ex[c] = scale_exponent(m[c]);
+      inv[c] = inverse_scale(ex[c]);
+    }
+    uint32_t words[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      words[r] = to_e4m3x4(lo(u[r].x) * inv[0], hi(u[r].x) * inv[1], lo(u[r].y) * inv[2],
+                           hi(u[r].y) * inv[3], 1.0f);
+    put_transposed(tile, words, warp, lane);
+    if (warp == 0 && col < d) {
+      const uint32_t bytes = static_cast<uint32_t>(ex[0] + 127) | (static_cast<uint32_t>(ex[1] + 127) << 8) |
+                             (static_cast<uint32_t>(ex[2] + 127) << 16) | (static_cast<uint32_t>(ex[3] + 127) << 24);
+      *reinterpret_cast<uint32_t*>(scales + static_cast<int64_t>(b) * d + col) = bytes;
+    }
+    __syncthreads();
+    write_transposed(tile, qt + static_cast<int64_t>(c0) * cap + static_cast<int64_t>(b) * 128, cap,
+                     min(128, d - c0), 128);
+    __syncthreads();                              // tile and col_max are free again
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_quantize_rows(const uint16_t* x, int64_t tokens, int d, const int32_t* pos,
+                                     int k, int64_t rows, uint8_t* q, uint8_t* scales, int* err,
+                                     cudaStream_t s) {
+  const int blocks = (d + kFp8Block - 1) / kFp8Block;
+  const int64_t grid = (tokens * blocks * 16 + kRowThreads - 1) / kRowThreads;
+  return launch_pdl(quantize_rows_kernel, dim3(static_cast<unsigned>(grid)), dim3(kRowThreads), 0, s,
+                    x, tokens, d, blocks, pos, k, rows, q, scales, err);
+}
+
+cudaError_t launch_fp8_quantize_blocks(const void* w, bool bf16, int experts, int n, int k,
+                                       uint8_t* q, uint8_t* scales, uint8_t* qt, uint8_t* scales_t,
+                                       int* err, cudaStream_t s) {
+  const int64_t grid = int64_t(experts) * ((n + 127) / 128) * ((k + 127) / 128);
+  const dim3 g(static_cast<unsigned>(grid)), b(kTileThreads);
+  if (bf16)
+    return launch_pdl(quantize_blocks_kernel<true>, g, b, 0, s, w, n, k, q, scales, qt, scales_t, err);
+  return launch_pdl(quantize_blocks_kernel<false>, g, b, 0, s, w, n, k, q, scales, qt, scales_t, err);
+}
+
+cudaError_t launch_fp8_quantize_cols(const uint16_t* x, int64_t x_rows, int d,
+                                     const int32_t* offsets, int experts, const int32_t* slots,
+                                     int top_k, int64_t rows, uint8_t* qt, int64_t cap,
+                                     uint8_t* scales, int* err, int num_sms, cudaStream_t s) {
+  const int64_t tiles = (cap / 128) * ((d + 127) / 128);
+  const int64_t grid = tiles < 4 * num_sms ? tiles : 4 * num_sms;
+  return launch_pdl(quantize_cols_kernel, dim3(static_cast<unsigned>(grid)), dim3(kTileThreads), 0, s,
+                    x, x_rows, d, offsets, experts, slots, top_k, rows, qt, cap, scales, err);
+}
+
+}  // namespace muon

@@ -10,6 +10,8 @@ namespace muon {
 // Device error bits written by kernels into the handle's flag word.
 constexpr int kDevErrTimeout = 1;
 constexpr int kDevErrNonFinite = 2;
+constexpr int kDevErrInput = 4;   // NaN or infinity in router logits or quantiser input
+constexpr int kDevErrIndex = 8;   // an expert id, row or offset out of range
 
 // Limits shared by every entry point: the longest matrix side, the
 // iteration count, and the largest grid.y of the elementwise kernels (one
@@ -129,6 +131,9 @@ cudaError_t launch_bounded_wait_selftest(int* err, uint64_t limit_ns, cudaStream
 
 // Last error text of a tensor-map encode (host, thread-local).
 const char* ns_last_encode_error();
+
+// cuTensorMapEncodeTiled of the installed driver (NULL: unavailable).
+void* tensor_map_encoder();
 
 // CTA-pair (cta_group::2) variants of the three products, 256 x 256 tiles;
 // the tensor maps are built by the ns_launch_* functions above (`_t`

@@ -25,7 +25,9 @@
 #include <vector>
 
 #include "muon.h"
+#include "handle.h"
 #include "kernels.h"
+#include "moe.h"
 
 namespace {
 
@@ -234,27 +236,7 @@ cudaEvent_t get_event(muon_handle_t h) {
 }
 
 // Brackets one kernel launch for accounting and (optionally) timing.
-struct LaunchScope {
-  muon_handle_t h;
-  int kind;
-  cudaStream_t s;
-  cudaEvent_t a = nullptr;
-  LaunchScope(muon_handle_t h_, int kind_, cudaStream_t s_) : h(h_), kind(kind_), s(s_) {
-    if (h->timing) {
-      a = get_event(h);
-      cudaEventRecord(a, s);
-    }
-  }
-  ~LaunchScope() {
-    h->stats.launches[kind] += 1;
-    h->stats.total_launches += 1;
-    if (h->timing && a != nullptr) {
-      cudaEvent_t b = get_event(h);
-      cudaEventRecord(b, s);
-      h->pending.push_back({kind, a, b});
-    }
-  }
-};
+using LaunchScope = muon::LaunchMark;
 
 muon_status_t ensure_workspace(muon_handle_t h, size_t bytes) {
   if (h->ws_size >= bytes) return MUON_OK;
@@ -360,6 +342,38 @@ int report(int status, const char* msg) {
   g_last_error = msg;
   return status;
 }
+
+int handle_info(muon_handle_s* h, HandleInfo* out) {
+  const muon_status_t st = check_handle(h);
+  if (st != MUON_OK) return st;
+  out->num_sms = h->num_sms;
+  out->dev_err = h->dev_err;
+  return MUON_OK;
+}
+
+int handle_workspace(muon_handle_s* h, size_t bytes, void** out) {
+  const muon_status_t st = ensure_workspace(h, bytes);
+  *out = h->ws;
+  return st;
+}
+
+LaunchMark::LaunchMark(muon_handle_s* h, int kind, cudaStream_t s)
+    : h_(h), kind_(kind), s_(s), a_(nullptr) {
+  if (h_->timing) {
+    a_ = get_event(h_);
+    cudaEventRecord(a_, s_);
+  }
+}
+
+LaunchMark::~LaunchMark() {
+  h_->stats.launches[kind_] += 1;
+  h_->stats.total_launches += 1;
+  if (a_ != nullptr) {
+    cudaEvent_t b = get_event(h_);
+    cudaEventRecord(b, s_);
+    h_->pending.push_back({kind_, a_, b});
+  }
+}
 }  // namespace muon
 
 // ======================================================================== ABI
@@ -408,6 +422,8 @@ muon_status_t muon_create(muon_handle_t* out, int32_t device, size_t workspace_b
   e = cudaSetDevice(device);
   if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
   e = muon::ns_gemm_init();
+  if (e == cudaSuccess) e = muon::moe_plan_init();
+  if (e == cudaSuccess) e = muon::fp8_gemm_init();
   if (e != cudaSuccess) return cuda_fail(e, "kernel attribute setup");
   muon_handle_t h = new muon_handle_s();
   h->device = device;
@@ -1077,7 +1093,11 @@ muon_status_t muon_last_device_error(muon_handle_t h, void* stream) {
     cudaDeviceSynchronize();
   }
   if (flag & muon::kDevErrTimeout) return fail(MUON_ERR_TIMEOUT, "a device-side wait expired");
+  if (flag & muon::kDevErrIndex)
+    return fail(MUON_ERR_INVALID_ARG, "an expert id, row or offset read on the device was out of range");
   if (flag & muon::kDevErrNonFinite) return fail(MUON_ERR_NONFINITE, "non-finite momentum norm");
+  if (flag & muon::kDevErrInput)
+    return fail(MUON_ERR_NONFINITE, "non-finite router logit or quantiser input");
   return MUON_OK;
 }
 

@@ -310,7 +310,54 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
       : "memory");
 }
 
+// ---------------------------------------------------------------- FP8, block scales
+// D[tmem] (+)= (A * 2^sa) * (B * 2^sb) for a CTA pair: 8-bit floats, one E8M0
+// scale per row of A (column of B) and 32 K values, scales in TMEM.
+__device__ __forceinline__ void tc_mma_mxf8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t sa_tmem,
+                                                 uint32_t sb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+      : "memory");
+}
+
+// 32 rows x 16 bytes from shared memory (each CTA's own) to four TMEM columns
+// of both CTAs of the pair, repeated in every 32-lane quarter: the layout of
+// 128 rows' scales.  Executes in order with this thread's MMAs.
+__device__ __forceinline__ void tc_copy_scales_pair(uint32_t taddr, uint64_t s_desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc)
+               : "memory");
+}
+
+// TMA store of a 3-D FP32 box that adds to what is there.
+__device__ __forceinline__ void tma_reduce_add_3d(const void* tmap, const void* smem_src,
+                                                  int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}],"
+      " [%1];" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+      "r"(smem_addr(smem_src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 // ---------------------------------------------------------------- descriptors
+// Shared-memory descriptor of 8-row x 16-byte core matrices without swizzle,
+// 128 bytes from one to the next (the scales' layout).
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (8ull << 32) | (1ull << 46);
+}
+
+// Instruction descriptor for kind::mxf8f6f4 with e4m3 A and B (both K-major),
+// E8M0 scales, scale byte 0 of each 32-bit TMEM cell.
+__host__ __device__ constexpr uint32_t idesc_mxf8(uint32_t M, uint32_t N) {
+  return ((N >> 3) << 17)     // N / 8
+         | (1u << 23)         // scale type: E8M0
+         | ((M >> 4) << 24);  // M / 16
+}
+
 // Shared-memory matrix descriptor (tcgen05 layout): start address, leading
 // and stride byte offsets (all >> 4), descriptor version 1 at bit 46, and
 // the swizzle mode in bits 61..63 (2 = 128-byte swizzle).
