@@ -16,11 +16,12 @@
 // (2 x 224 + 32 <= 512 columns).
 //
 // The tensor cores multiply by the scales: each 128-wide K block is four MMAs
-// (K = 32) that read one scale byte per row of A and of B from TMEM.  Scales
-// travel as bytes: two warps per CTA gather the block's 128 + up to 256 bytes,
-// spread them to the 32-bit cells TMEM wants in shared memory, and the MMA
-// thread copies them over (tcgen05.cp) ahead of the block's MMAs.  Every
-// K block has its own cells, so no alignment of the rows is needed.
+// (K = 32) that read one scale byte per row of A and of B from TMEM, where a
+// 32-bit cell holds the bytes of four K blocks.  Two warps per CTA gather four
+// blocks' bytes of the tile's rows at a time (a set), with the next set's loads
+// in flight, write them to a ring in shared memory apart from the operands',
+// and the MMA thread copies a set to TMEM (tcgen05.cp) ahead of its MMAs.  Sets
+// are counted from the tile's first K block, so rows need no alignment.
 //
 // A persistent pair walks the tiles.  Warp 0: TMA producer.  Warp 1: TMEM and,
 // in the even CTA, the MMAs.  Warps 2-5: epilogue, overlapped with the next
@@ -48,13 +49,15 @@ constexpr int kHalfM = 128;
 constexpr int kBK = 128;                          // K block: one 128-byte swizzle row, one scale
 constexpr int kABytes = kHalfM * kBK;             // 16 KB per CTA and stage
 constexpr int kStages = 6;
-constexpr int kScaleBytes = 512 + 1024;           // per stage: 128 A cells, 256 B cells
+constexpr int kSetBlocks = 4;                     // K blocks per set of scales
+constexpr int kSets = 4;                          // sets in the ring
+constexpr int kScaleBytes = 512 + 1024;           // per set: 128 A cells, 256 B cells
 constexpr int kMaxTokens = 224;                   // rows: widest token tile
 constexpr int kWidthUnit = 32;                    // MMA columns come in multiples of this
 constexpr int kGradN = 192;                       // wgrad: columns per tile (a multiple of 32)
 constexpr int kTokenGroup = 8;                    // rows: token tiles that share a sweep over w
 constexpr int kTmemCols = 512;
-constexpr int kTmemScales = 480;
+constexpr int kTmemScales = 448;
 constexpr int kMaps = kMaxTokens / kWidthUnit;    // B boxes: half a width each
 
 template <bool GRAD>
@@ -64,7 +67,7 @@ struct Layout {
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kOutBuf = GRAD ? 4096 : 2048;          // one 32 x 32 chunk
   static constexpr int kScaleAt = kStages * kStageBytes;
-  static constexpr int kOutAt = kScaleAt + kStages * kScaleBytes;
+  static constexpr int kOutAt = kScaleAt + kSets * kScaleBytes;
   static constexpr int kTableAt = kOutAt + kEpiWarps * 2 * kOutBuf;
   static constexpr int kTableBytes = (kMoeMaxExperts + 4) * 4;
   static constexpr int kBarAt = kTableAt + 2 * kTableBytes;
@@ -204,6 +207,96 @@ __device__ __forceinline__ void scan_experts(const Fp8Args& p, int32_t* first, i
   if (bad && blockIdx.x == 0) atomicOr(p.err, kDevErrIndex);
 }
 
+// Walks the sets of scales of a pair's tiles.
+struct SetCursor {
+  int64_t t;
+  Tile o;
+  int kb;               // first K block of the set
+  bool live;
+
+  template <bool GRAD>
+  __device__ __forceinline__ void begin(const Fp8Args& p, const int32_t* first, const int32_t* start,
+                                        int64_t t0) {
+    t = t0;
+    kb = 0;
+    live = decode<GRAD>(p, first, start, t, o);
+  }
+  // Leaves a tile without K blocks at once.
+  template <bool GRAD>
+  __device__ __forceinline__ void settle(const Fp8Args& p, const int32_t* first,
+                                         const int32_t* start, int step) {
+    while (live && kb >= o.nkb) {
+      t += step;
+      kb = 0;
+      live = decode<GRAD>(p, first, start, t, o);
+    }
+  }
+  template <bool GRAD>
+  __device__ __forceinline__ void next(const Fp8Args& p, const int32_t* first, const int32_t* start,
+                                       int step) {
+    kb += kSetBlocks;
+    settle<GRAD>(p, first, start, step);
+  }
+};
+
+// A row's scale bytes of K blocks kb .. kb + 3 (below `end`), byte 0 first.
+__device__ __forceinline__ uint32_t four_along(const uint8_t* row, int kb, int end, bool words) {
+  if (words) return __ldg(reinterpret_cast<const uint32_t*>(row + kb));
+  uint32_t v = 0u;
+#pragma unroll
+  for (int i = 0; i < kSetBlocks; ++i)
+    if (kb + i < end) v |= static_cast<uint32_t>(__ldg(row + kb + i)) << (8 * i);
+  return v;
+}
+
+__device__ __forceinline__ uint32_t four_across(const uint8_t* at, int64_t pitch, int n) {
+  uint32_t v = 0u;
+#pragma unroll
+  for (int i = 0; i < kSetBlocks; ++i)
+    if (i < n) v |= static_cast<uint32_t>(__ldg(at + i * pitch)) << (8 * i);
+  return v;
+}
+
+// This lane's cells of one set: rows lane + 32 i, four of A's, eight of B's.
+template <bool GRAD>
+__device__ __forceinline__ void load_set(const Fp8Args& p, const SetCursor& s, uint32_t rank,
+                                         int lane, uint32_t (&cells)[12]) {
+  const Tile& o = s.o;
+  const int row_a = o.n0 + static_cast<int>(rank) * kHalfM;
+  if (GRAD) {
+    const int64_t kb = o.kb0 + s.kb;
+    const int n = o.nkb - s.kb;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = row_a + i * 32 + lane;
+      cells[i] = r < p.n ? four_across(p.a_scales + kb * p.n + r, p.n, n) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = o.c0 + i * 32 + lane;
+      cells[4 + i] = i * 32 < kGradN && c < p.k ? four_across(p.b_scales + kb * p.k + c, p.k, n) : 0u;
+    }
+  } else {
+    // Rows of a multiple of four blocks start on a word: the buffers are
+    // 16-byte aligned.
+    const bool words = p.k_blocks % kSetBlocks == 0;
+    uint32_t w = 0u;
+    if (row_a < p.n)
+      w = four_along(p.a_scales + (static_cast<int64_t>(o.expert) * p.n_blocks + row_a / kBK) * p.k_blocks,
+                     s.kb, o.nkb, words);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cells[i] = w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = i * 32 + lane;
+      cells[4 + i] = 0u;
+      if (c < o.cols)
+        cells[4 + i] = four_along(p.b_scales + static_cast<int64_t>(o.c0 + c) * p.k_blocks, s.kb,
+                                  o.nkb, words);
+    }
+  }
+}
+
 template <bool GRAD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp8_product_kernel(const __grid_constant__ Maps maps, const Fp8Args p) {
@@ -215,7 +308,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int32_t* start = reinterpret_cast<int32_t*>(smem + L::kTableAt + L::kTableBytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBarAt);
   uint64_t* empty = full + kStages;
-  uint64_t* tmem_full = empty + kStages;
+  uint64_t* set_full = empty + kStages;
+  uint64_t* set_empty = set_full + kSets;
+  uint64_t* tmem_full = set_empty + kSets;
   uint64_t* tmem_empty = tmem_full + 2;
   uint64_t* drain = tmem_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
@@ -231,8 +326,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      ptx::mbar_init(&full[s], 1 + 2);            // the TMA bytes, both CTAs' scales
+      ptx::mbar_init(&full[s], 1);
       ptx::mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kSets; ++s) {
+      ptx::mbar_init(&set_full[s], 2);            // both CTAs' scales
+      ptx::mbar_init(&set_empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(&tmem_full[a], 1);
@@ -314,7 +413,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
-      uint32_t cells = 0;
+      int set = 0;
+      uint32_t set_phase = 0;
       bool ok = true;
       Tile o;
       for (int64_t t = pair; ok && decode<GRAD>(p, first, start, t, o); t += npairs) {
@@ -325,20 +425,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         ptx::tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * L::kAccCols);
-        const uint32_t idesc = ptx::idesc_mxf8(kTileM, o.width);
+        const uint32_t idesc0 = ptx::idesc_mxf8(kTileM, o.width);
         for (int kb = 0; kb < o.nkb; ++kb) {
+          // Two sets of scale cells in TMEM in turn.
+          const uint32_t sa_tmem = tmem_base + kTmemScales + (set & 1) * 16, sb_tmem = sa_tmem + 4;
+          const int in_set = kb % kSetBlocks;
+          if (in_set == 0) {
+            if (!ptx::mbar_wait_cluster(&set_full[set], set_phase, abort_flag)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t ss = ptx::smem_addr(smem + L::kScaleAt + set * kScaleBytes);
+            ptx::tc_copy_scales_pair(sa_tmem, ptx::smem_desc_scales(ss));
+            ptx::tc_copy_scales_pair(sb_tmem, ptx::smem_desc_scales(ss + 512));
+            if (o.width > 128)
+              ptx::tc_copy_scales_pair(sb_tmem + 4, ptx::smem_desc_scales(ss + 1024));
+          }
           if (!ptx::mbar_wait_cluster(&full[stage], phase, abort_flag)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          // Two sets of scale cells in turn.
-          const uint32_t sa_tmem = tmem_base + kTmemScales + cells * 16, sb_tmem = sa_tmem + 4;
-          cells ^= 1u;
-          const uint32_t ss = ptx::smem_addr(smem + L::kScaleAt + stage * kScaleBytes);
-          ptx::tc_copy_scales_pair(sa_tmem, ptx::smem_desc_scales(ss));
-          ptx::tc_copy_scales_pair(sb_tmem, ptx::smem_desc_scales(ss + 512));
-          if (o.width > 128) ptx::tc_copy_scales_pair(sb_tmem + 4, ptx::smem_desc_scales(ss + 1024));
+          const uint32_t idesc = ptx::idesc_mxf8_byte(idesc0, in_set);
           const uint32_t sa = ptx::smem_addr(smem + stage * L::kStageBytes);
           const uint32_t sb = sa + kABytes;
 #pragma unroll
@@ -350,6 +459,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1u;
+          }
+          if (in_set == kSetBlocks - 1 || kb == o.nkb - 1) {
+            ptx::tc_commit_pair_multicast(&set_empty[set], 0x3);
+            if (++set == kSets) {
+              set = 0;
+              set_phase ^= 1u;
+            }
           }
         }
         if (!ok) break;
@@ -452,62 +568,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ scales (both CTAs)
-    const int which = warp - 2 - kEpiWarps;       // K blocks which, which + 2, ...
-    int stage = 0;
-    uint32_t phase = 0;
-    uint32_t turn = 0;
+    // Warp `which` fills the sets which, which + 2, ...; the loads of its next
+    // set are in flight while the current one waits for its place.
+    const int which = warp - 2 - kEpiWarps;
+    SetCursor at{};
+    at.begin<GRAD>(p, first, start, pair);
+    at.settle<GRAD>(p, first, start, npairs);
+    if (which == 1 && at.live) at.next<GRAD>(p, first, start, npairs);
+    uint32_t cells[12];
+    if (at.live) load_set<GRAD>(p, at, rank, lane, cells);
+    int set = which;
+    uint32_t set_phase = 0;
     bool ok = true;
-    Tile o;
-    for (int64_t t = pair; ok && decode<GRAD>(p, first, start, t, o); t += npairs) {
-      const int row_a = o.n0 + static_cast<int>(rank) * kHalfM;
-      for (int kb = 0; kb < o.nkb; ++kb) {
-        if (turn == static_cast<uint32_t>(which)) {
-          uint32_t a[4], b[8];
-          const int64_t at = o.kb0 + kb;
-          if (GRAD) {
+    while (at.live) {
+      uint32_t now[12];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = row_a + i * 32 + lane;
-              a[i] = r < p.n ? __ldg(p.a_scales + at * p.n + r) : 127u;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int c = o.c0 + i * 32 + lane;
-              b[i] = i * 32 < kGradN && c < p.k ? __ldg(p.b_scales + at * p.k + c) : 127u;
-            }
-          } else {
-            const uint32_t w =
-                row_a < p.n ? __ldg(p.a_scales + (static_cast<int64_t>(o.expert) * p.n_blocks +
-                                                  row_a / kBK) * p.k_blocks + at)
-                            : 127u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = w;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int c = i * 32 + lane;
-              b[i] = c < o.cols ? __ldg(p.b_scales + static_cast<int64_t>(o.c0 + c) * p.k_blocks + at)
-                                : 127u;
-            }
-          }
-          const bool got = ptx::mbar_wait_cluster(&empty[stage], phase ^ 1u, abort_flag);
-          if (!__all_sync(0xffffffffu, got)) {
-            ok = false;
-            break;
-          }
-          // Lane l's 16 bytes hold the cells of rows l, l + 32, l + 64, l + 96.
-          uint4* cells = reinterpret_cast<uint4*>(smem + L::kScaleAt + stage * kScaleBytes);
-          cells[lane] = make_uint4(a[0], a[1], a[2], a[3]);
-          cells[32 + lane] = make_uint4(b[0], b[1], b[2], b[3]);
-          cells[64 + lane] = make_uint4(b[4], b[5], b[6], b[7]);
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&full[stage]), 0));
-        }
-        turn ^= 1u;
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+      for (int i = 0; i < 12; ++i) now[i] = cells[i];
+      at.next<GRAD>(p, first, start, npairs);
+      if (at.live) at.next<GRAD>(p, first, start, npairs);
+      if (at.live) load_set<GRAD>(p, at, rank, lane, cells);
+      const bool got = ptx::mbar_wait_cluster(&set_empty[set], set_phase ^ 1u, abort_flag);
+      if (!__all_sync(0xffffffffu, got)) {
+        ok = false;
+        break;
+      }
+      // Lane l's 16 bytes hold the cells of rows l, l + 32, l + 64, l + 96.
+      uint4* to = reinterpret_cast<uint4*>(smem + L::kScaleAt + set * kScaleBytes);
+      to[lane] = make_uint4(now[0], now[1], now[2], now[3]);
+      to[32 + lane] = make_uint4(now[4], now[5], now[6], now[7]);
+      to[64 + lane] = make_uint4(now[8], now[9], now[10], now[11]);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&set_full[set]), 0));
+      set += 2;
+      if (set >= kSets) {
+        set -= kSets;
+        set_phase ^= 1u;
       }
     }
     if (!ok && lane == 0) {

@@ -351,11 +351,14 @@ __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
 }
 
 // Instruction descriptor for kind::mxf8f6f4 with e4m3 A and B (both K-major),
-// E8M0 scales, scale byte 0 of each 32-bit TMEM cell.
+// E8M0 scales, scale byte 0 of each 32-bit TMEM cell; and with byte `b`.
 __host__ __device__ constexpr uint32_t idesc_mxf8(uint32_t M, uint32_t N) {
   return ((N >> 3) << 17)     // N / 8
          | (1u << 23)         // scale type: E8M0
          | ((M >> 4) << 24);  // M / 16
+}
+__host__ __device__ constexpr uint32_t idesc_mxf8_byte(uint32_t idesc, uint32_t b) {
+  return idesc | (b << 4) | (b << 29);
 }
 
 // Shared-memory matrix descriptor (tcgen05 layout): start address, leading
