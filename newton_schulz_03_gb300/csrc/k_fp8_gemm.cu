@@ -408,7 +408,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (lane == 0 && leader) {
+    // The whole warp walks the loop and one elected lane issues: addresses and
+    // descriptors are then the same in all lanes and stay in uniform
+    // registers, where these instructions want them.
+    if (leader) {
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -416,6 +419,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int set = 0;
       uint32_t set_phase = 0;
       bool ok = true;
+      const uint64_t a_desc0 = ptx::smem_desc_sw128(ptx::smem_addr(smem), 16, 1024);
+      const uint64_t s_desc0 = ptx::smem_desc_scales(ptx::smem_addr(smem + L::kScaleAt));
       Tile o;
       for (int64_t t = pair; ok && decode<GRAD>(p, first, start, t, o); t += npairs) {
         if (o.nkb == 0) continue;
@@ -426,58 +431,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * L::kAccCols);
         const uint32_t idesc0 = ptx::idesc_mxf8(kTileM, o.width);
-        for (int kb = 0; kb < o.nkb; ++kb) {
-          // Two sets of scale cells in TMEM in turn.
-          const uint32_t sa_tmem = tmem_base + kTmemScales + (set & 1) * 16, sb_tmem = sa_tmem + 4;
-          const int in_set = kb % kSetBlocks;
-          if (in_set == 0) {
-            if (!ptx::mbar_wait_cluster(&set_full[set], set_phase, abort_flag)) {
-              ok = false;
-              break;
-            }
-            ptx::tc_fence_after();
-            const uint32_t ss = ptx::smem_addr(smem + L::kScaleAt + set * kScaleBytes);
-            ptx::tc_copy_scales_pair(sa_tmem, ptx::smem_desc_scales(ss));
-            ptx::tc_copy_scales_pair(sb_tmem, ptx::smem_desc_scales(ss + 512));
-            if (o.width > 128)
-              ptx::tc_copy_scales_pair(sb_tmem + 4, ptx::smem_desc_scales(ss + 1024));
-          }
-          if (!ptx::mbar_wait_cluster(&full[stage], phase, abort_flag)) {
+        const bool wide = o.width > 128;
+        for (int kb0 = 0; ok && kb0 < o.nkb; kb0 += kSetBlocks) {
+          if (!ptx::mbar_wait_cluster(&set_full[set], set_phase, abort_flag)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t idesc = ptx::idesc_mxf8_byte(idesc0, in_set);
-          const uint32_t sa = ptx::smem_addr(smem + stage * L::kStageBytes);
-          const uint32_t sb = sa + kABytes;
-#pragma unroll
-          for (int k = 0; k < kBK / 32; ++k)
-            ptx::tc_mma_mxf8_pair(d_tmem, ptx::smem_desc_sw128(sa + k * 32, 16, 1024),
-                                  ptx::smem_desc_sw128(sb + k * 32, 16, 1024), idesc, sa_tmem,
-                                  sb_tmem, (kb | k) != 0 ? 1u : 0u);
-          ptx::tc_commit_pair_multicast(&empty[stage], 0x3);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
+          // Two sets of scale cells in TMEM in turn.
+          const uint32_t sa_tmem = tmem_base + kTmemScales + (set & 1) * 16, sb_tmem = sa_tmem + 4;
+          const uint64_t s_desc = s_desc0 + static_cast<uint32_t>(set * (kScaleBytes >> 4));
+          if (ptx::elect_one()) {
+            ptx::tc_copy_scales_pair(sa_tmem, s_desc);
+            ptx::tc_copy_scales_pair(sb_tmem, s_desc + (512 >> 4));
+            if (wide) ptx::tc_copy_scales_pair(sb_tmem + 4, s_desc + (1024 >> 4));
           }
-          if (in_set == kSetBlocks - 1 || kb == o.nkb - 1) {
-            ptx::tc_commit_pair_multicast(&set_empty[set], 0x3);
-            if (++set == kSets) {
-              set = 0;
-              set_phase ^= 1u;
+          __syncwarp();
+#pragma unroll
+          for (int b = 0; b < kSetBlocks; ++b) {
+            if (kb0 + b >= o.nkb) break;
+            if (!ptx::mbar_wait_cluster(&full[stage], phase, abort_flag)) {
+              ok = false;
+              break;
             }
+            ptx::tc_fence_after();
+            const uint32_t idesc = ptx::idesc_mxf8_byte(idesc0, b);
+            const uint64_t a_desc = a_desc0 + static_cast<uint32_t>(stage * (L::kStageBytes >> 4));
+            const uint64_t b_desc = a_desc + (kABytes >> 4);
+            if (ptx::elect_one()) {
+#pragma unroll
+              for (int k = 0; k < kBK / 32; ++k)
+                ptx::tc_mma_mxf8_pair(d_tmem, a_desc + k * 2, b_desc + k * 2, idesc, sa_tmem, sb_tmem,
+                                      (kb0 | b | k) != 0 ? 1u : 0u);
+              ptx::tc_commit_pair_multicast(&empty[stage], 0x3);
+            }
+            __syncwarp();
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (!ok) break;
+          if (ptx::elect_one()) ptx::tc_commit_pair_multicast(&set_empty[set], 0x3);
+          __syncwarp();
+          if (++set == kSets) {
+            set = 0;
+            set_phase ^= 1u;
           }
         }
         if (!ok) break;
-        ptx::tc_commit_pair_multicast(&tmem_full[acc], 0x3);
+        if (ptx::elect_one()) ptx::tc_commit_pair_multicast(&tmem_full[acc], 0x3);
+        __syncwarp();
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         *abort_flag = 1;
         atomicOr(p.err, kDevErrTimeout);
       }
-      ptx::tc_commit_pair(drain);
+      if (ptx::elect_one()) ptx::tc_commit_pair(drain);
+      __syncwarp();
       ptx::mbar_wait(drain, 0, nullptr);
     }
   } else if (warp < 2 + kEpiWarps) {
