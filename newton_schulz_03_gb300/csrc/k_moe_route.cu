@@ -81,8 +81,8 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// The same operations as 1 / (1 + exp(-x)) written out in FP32.
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// 1 / (1 + exp(-x)), each operation rounded to FP32.
+__device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(1.0f + expf(-x)); }
 
 __device__ __forceinline__ bool is_open(float x) { return fabsf(x) <= FLT_MAX; }
 
@@ -116,9 +116,138 @@ __device__ __forceinline__ void warp_best(uint32_t& key, int& e) {
   key = top;
 }
 
+// Values of the groups, group g's in lane g: the ordered sum of its best
+// group_top open experts' choice values, 0 where none is open.
+__device__ __forceinline__ uint32_t group_key(uint32_t first, uint32_t second, int group_top) {
+  if (first == 0u) return 0u;
+  const float f = unordered(first);
+  return ordered(group_top == 2 && second != 0u ? f + unordered(second) : f);
+}
+
+// Groups of `lanes` = 1, 2, 4 .. 32 neighbouring lanes of a vector: the best
+// two by a butterfly, then every group's key to its lane.
+template <int R>
+__device__ __forceinline__ uint32_t group_keys_by_lanes(const uint32_t (&key)[R], int lanes,
+                                                        int groups, int group_top, int lane) {
+  const int per_vector = 32 / lanes;              // groups in one vector of 128 experts
+  uint32_t mine = 0u;
+#pragma unroll
+  for (int i = 0; i < R / 4; ++i) {
+    if (i * per_vector >= groups) break;
+    const uint32_t a = key[4 * i], b = key[4 * i + 1], c = key[4 * i + 2], d = key[4 * i + 3];
+    const uint32_t hi0 = max(a, b), lo0 = min(a, b), hi1 = max(c, d), lo1 = min(c, d);
+    uint32_t first = max(hi0, hi1);
+    uint32_t second = max(min(hi0, hi1), hi0 > hi1 ? lo0 : lo1);
+    for (int o = 1; o < lanes; o <<= 1) {
+      const uint32_t f = __shfl_xor_sync(kAll, first, o), q = __shfl_xor_sync(kAll, second, o);
+      second = max(min(first, f), max(second, q));
+      first = max(first, f);
+    }
+    const uint32_t g = __shfl_sync(kAll, group_key(first, second, group_top),
+                                   (lane % per_vector) * lanes);
+    if (lane / per_vector == i) mine = g;
+  }
+  return lane < groups ? mine : 0u;
+}
+
+// Any group size: lane g walks group g in shared memory, each lane starting
+// elsewhere (distinct banks).
+__device__ __forceinline__ uint32_t group_keys_by_walk(const uint32_t* keys, int size, int groups,
+                                                       int group_top, int lane) {
+  if (lane >= groups) return 0u;
+  uint32_t first = 0u, second = 0u;
+  int j = lane % size;
+  for (int i = 0; i < size; ++i) {
+    const uint32_t v = keys[lane * size + j];
+    second = max(second, min(first, v));
+    first = max(first, v);
+    if (++j == size) j = 0;
+  }
+  return group_key(first, second, group_top);
+}
+
+// The k largest of key[0 .. used) over the warp, ties to the lowest expert;
+// returns the j-th one's expert in lane j (-1: fewer than k are open).  A
+// lane's keys lie in order of expert.  The k-th largest of the lanes' maxima is
+// a lower bound of the k-th largest key: only the few keys that reach it are
+// gathered, one per lane, and ranked by counting.
+template <int R>
+__device__ __forceinline__ int choose(uint32_t (&key)[R], const int (&expert)[R], int used, int k,
+                                      int lane, uint2* list) {
+  uint32_t most = 0u;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (r < used) most = max(most, key[r]);
+  uint32_t bound = 1u, left = most;               // no closed expert reaches 1
+  for (int got = 0; got < k;) {
+    const uint32_t top = __reduce_max_sync(kAll, left);
+    if (top == 0u) {
+      bound = 1u;
+      break;
+    }
+    bound = top;
+    const bool is_top = left == top;
+    got += __popc(__ballot_sync(kAll, is_top));
+    if (is_top) left = 0u;
+  }
+  // Places of this lane's candidates.
+  int mine = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (r < used) mine += key[r] >= bound ? 1 : 0;
+  int end = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kAll, end, o);
+    if (lane >= o) end += v;
+  }
+  const int total = __shfl_sync(kAll, end, 31);
+  if (total <= 32) {
+    int at = end - mine;
+    if (mine > 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (r < used && key[r] >= bound) list[at++] = make_uint2(key[r], static_cast<uint32_t>(expert[r]));
+    }
+    __syncwarp();
+    uint2 own = make_uint2(0u, 0u);
+    if (lane < total) own = list[lane];
+    int rank = 0;
+    for (int j = 0; j < total; ++j) {
+      const uint2 other = list[j];
+      rank += other.x > own.x || (other.x == own.x && other.y < own.y) ? 1 : 0;
+    }
+    __syncwarp();
+    if (lane < total) list[rank].y = own.y;       // ranks are distinct
+    __syncwarp();
+    return lane < min(k, total) ? static_cast<int>(list[lane].y) : -1;
+  }
+  // Many equal keys: k rounds of the warp's best one.
+  int id = -1;
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = 0u;
+    int e = INT32_MAX;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r < used && key[r] > best) {
+        best = key[r];
+        e = expert[r];
+      }
+    warp_best(best, e);
+    if (best == 0u) break;
+    if (lane == j) id = e;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r < used && expert[r] == e) key[r] = 0u;
+  }
+  return id;
+}
+
 template <typename T, int V, int R>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
   extern __shared__ uint32_t smem_keys[];
+  __shared__ uint2 lists[kWarps][32];
+  __shared__ int group_list[kWarps][kMoeMaxGroups];
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -149,7 +278,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
     }
   }
   if (bad) atomicOr(a.err, kDevErrInput);
-  if (a.softmax) {
+  const bool by_logit = a.softmax && a.bias == nullptr && a.group_top == 1;
+  if (a.softmax && !(by_logit && a.renorm)) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
 #pragma unroll
@@ -159,45 +289,42 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
 
   // Choice values as ordered numbers.
   uint32_t key[R];
-  const bool by_logit = a.softmax && a.bias == nullptr && a.group_top == 1;
+  int expert[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
+    expert[r] = expert_of<V>(r, lane);
     key[r] = 0u;
     if (x[r] > -INFINITY) {
       float c = x[r];
       if (!by_logit) {
         c = a.softmax ? expf(x[r] - top) / denom : sigmoid(x[r]);
-        if (a.bias != nullptr) c += a.bias[expert_of<V>(r, lane)];
+        if (a.bias != nullptr) c += a.bias[expert[r]];
       }
       key[r] = c == c ? ordered(c) : 0u;
     }
   }
+  int used = R;
 
   if (a.groups > 1) {
-    // Lane g values group g: the sum of its best group_top open experts.
     uint32_t* keys = smem_keys + warp * a.experts;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < R; r += V) {
       const int e = expert_of<V>(r, lane);
-      if (e < a.experts) keys[e] = key[r];
+      if (e >= a.experts) continue;
+      if (V == 4)
+        *reinterpret_cast<uint4*>(keys + e) =
+            make_uint4(key[r], key[(r + 1) % R], key[(r + 2) % R], key[(r + 3) % R]);
+      else
+        keys[e] = key[r];
     }
     __syncwarp();
     const int size = a.experts / a.groups;
-    uint32_t gkey = 0u;
-    if (lane < a.groups) {
-      uint32_t first = 0u, second = 0u;
-      int j = lane % size;               // each lane starts elsewhere: distinct banks
-      for (int i = 0; i < size; ++i) {
-        const uint32_t v = keys[lane * size + j];
-        second = max(second, min(first, v));
-        first = max(first, v);
-        if (++j == size) j = 0;
-      }
-      if (first != 0u) {
-        const float f = unordered(first);
-        gkey = ordered(a.group_top == 2 && second != 0u ? f + unordered(second) : f);
-      }
-    }
+    const int lanes = size / 4;                   // of a group within a vector
+    uint32_t gkey;
+    if (V == 4 && size % 4 == 0 && lanes <= 32 && (lanes & (lanes - 1)) == 0)
+      gkey = group_keys_by_lanes<R>(key, lanes, a.groups, a.group_top, lane);
+    else
+      gkey = group_keys_by_walk(keys, size, a.groups, a.group_top, lane);
     uint32_t stay = 0u;
     for (int i = 0; i < a.top_groups; ++i) {
       uint32_t best = gkey;
@@ -207,45 +334,23 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
       stay |= 1u << g;
       if (lane == g) gkey = 0u;
     }
+    // The groups' experts, in order, spread over the lanes anew.
+    if ((stay >> lane) & 1u) group_list[warp][__popc(stay & ((1u << lane) - 1u))] = lane;
+    __syncwarp();
+    const int n = __popc(stay) * size;
+    used = (n + 31) / 32;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int e = expert_of<V>(r, lane);
-      if (e < a.experts && !((stay >> (e / size)) & 1u)) key[r] = 0u;
-    }
-  }
-
-  // k rounds: each lane offers its best, the winner clears it and looks for
-  // its next one.
-  uint32_t best = 0u;
-  int best_r = 0;
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (key[r] > best) {
-      best = key[r];
-      best_r = r;
-    }
-  int my_id = -1;
-  for (int j = 0; j < a.k; ++j) {
-    uint32_t top_key = best;
-    const int mine = expert_of<V>(best_r, lane);
-    int e = mine;
-    warp_best(top_key, e);
-    if (top_key == 0u) break;
-    if (lane == j) my_id = e;
-    if (mine == e && best == top_key) {
-      best = 0u;
-      int next = 0;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (r == best_r) key[r] = 0u;
-        if (key[r] > best) {
-          best = key[r];
-          next = r;
-        }
+      if (r >= used) break;
+      const int c = r * 32 + lane, g = c / size;
+      key[r] = 0u;
+      if (c < n) {
+        expert[r] = group_list[warp][g] * size + (c - g * size);
+        key[r] = keys[expert[r]];
       }
-      best_r = next;
     }
   }
+  const int my_id = choose<R>(key, expert, used, a.k, lane, lists[warp]);
 
   // Lane j holds the j-th choice; its logit is in L1.
   float s = 0.f;
