@@ -166,18 +166,17 @@ __device__ __forceinline__ uint32_t group_keys_by_walk(const uint32_t* keys, int
   return group_key(first, second, group_top);
 }
 
-// The k largest of key[0 .. used) over the warp, ties to the lowest expert;
+// The k largest of the lanes' keys over the warp, ties to the lowest expert;
 // returns the j-th one's expert in lane j (-1: fewer than k are open).  A
 // lane's keys lie in order of expert.  The k-th largest of the lanes' maxima is
 // a lower bound of the k-th largest key: only the few keys that reach it are
 // gathered, one per lane, and ranked by counting.
 template <int R>
-__device__ __forceinline__ int choose(uint32_t (&key)[R], const int (&expert)[R], int used, int k,
-                                      int lane, uint2* list) {
+__device__ __forceinline__ int choose(uint32_t (&key)[R], const int (&expert)[R], int k, int lane,
+                                      uint2* list) {
   uint32_t most = 0u;
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (r < used) most = max(most, key[r]);
+  for (int r = 0; r < R; ++r) most = max(most, key[r]);
   uint32_t bound = 1u, left = most;               // no closed expert reaches 1
   for (int got = 0; got < k;) {
     const uint32_t top = __reduce_max_sync(kAll, left);
@@ -194,7 +193,7 @@ __device__ __forceinline__ int choose(uint32_t (&key)[R], const int (&expert)[R]
   int mine = 0;
 #pragma unroll
   for (int r = 0; r < R; ++r)
-    if (r < used) mine += key[r] >= bound ? 1 : 0;
+    mine += key[r] >= bound ? 1 : 0;
   int end = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -207,7 +206,7 @@ __device__ __forceinline__ int choose(uint32_t (&key)[R], const int (&expert)[R]
     if (mine > 0) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        if (r < used && key[r] >= bound) list[at++] = make_uint2(key[r], static_cast<uint32_t>(expert[r]));
+        if (key[r] >= bound) list[at++] = make_uint2(key[r], static_cast<uint32_t>(expert[r]));
     }
     __syncwarp();
     uint2 own = make_uint2(0u, 0u);
@@ -229,7 +228,7 @@ __device__ __forceinline__ int choose(uint32_t (&key)[R], const int (&expert)[R]
     int e = INT32_MAX;
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (r < used && key[r] > best) {
+      if (key[r] > best) {
         best = key[r];
         e = expert[r];
       }
@@ -238,9 +237,29 @@ __device__ __forceinline__ int choose(uint32_t (&key)[R], const int (&expert)[R]
     if (lane == j) id = e;
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (r < used && expert[r] == e) key[r] = 0u;
+      if (expert[r] == e) key[r] = 0u;
   }
   return id;
+}
+
+// choose() among the n experts of the listed groups (n <= 32 R).
+template <int R>
+__device__ __forceinline__ int choose_of(const uint32_t* keys, const int* groups, int size, int n,
+                                         int k, int lane, uint2* list) {
+  uint32_t key[R];
+  int expert[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int c = r * 32 + lane;
+    key[r] = 0u;
+    expert[r] = INT32_MAX;
+    if (c < n) {
+      const int g = c / size;
+      expert[r] = groups[g] * size + (c - g * size);
+      key[r] = keys[expert[r]];
+    }
+  }
+  return choose<R>(key, expert, k, lane, list);
 }
 
 template <typename T, int V, int R>
@@ -265,25 +284,33 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
   float x[R];
   load_row<T, V, R>(static_cast<const T*>(a.logits) + t * a.experts, a.experts, lane, x);
 
-  // Softmax statistics over the open experts.
-  float top = -INFINITY, denom = 0.f;
-  bool bad = false;
+  // Whether every logit is finite: x * 0 is NaN otherwise.
+  const bool whole = a.experts == 32 * R;
+  float z = 0.f;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (is_open(x[r])) {
-      top = fmaxf(top, x[r]);
-    } else {
-      bad = bad || !(x[r] < 0.f);     // NaN or +inf: closed, and reported
-      x[r] = -INFINITY;
-    }
+  for (int r = 0; r < R; ++r)
+    if (whole || expert_of<V>(r, lane) < a.experts) z = fmaf(x[r], 0.f, z);
+  const bool finite = __all_sync(kAll, z == 0.f);
+  if (!finite) {
+    bool bad = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (!is_open(x[r])) {
+        bad = bad || !(x[r] < 0.f);   // NaN or +inf: closed, and reported
+        x[r] = -INFINITY;
+      }
+    if (bad) atomicOr(a.err, kDevErrInput);
   }
-  if (bad) atomicOr(a.err, kDevErrInput);
+  // Softmax statistics; a closed expert's exp is 0.
+  float top = -FLT_MAX, denom = 0.f;
   const bool by_logit = a.softmax && a.bias == nullptr && a.group_top == 1;
   if (a.softmax && !(by_logit && a.renorm)) {
 #pragma unroll
+    for (int r = 0; r < R; ++r) top = fmaxf(top, x[r]);
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
 #pragma unroll
-    for (int r = 0; r < R; ++r) denom += x[r] > -INFINITY ? expf(x[r] - top) : 0.f;
+    for (int r = 0; r < R; ++r) denom += expf(x[r] - top);
     denom = warp_sum(denom);
   }
 
@@ -291,19 +318,32 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
   uint32_t key[R];
   int expert[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    expert[r] = expert_of<V>(r, lane);
-    key[r] = 0u;
-    if (x[r] > -INFINITY) {
-      float c = x[r];
-      if (!by_logit) {
-        c = a.softmax ? expf(x[r] - top) / denom : sigmoid(x[r]);
-        if (a.bias != nullptr) c += a.bias[expert[r]];
-      }
-      key[r] = c == c ? ordered(c) : 0u;
-    }
+  for (int r = 0; r < R; ++r) expert[r] = expert_of<V>(r, lane);
+  float c[R];
+  if (by_logit) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) c[r] = x[r];
+  } else if (a.softmax) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) c[r] = expf(x[r] - top) / denom;
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) c[r] = sigmoid(x[r]);
   }
-  int used = R;
+  if (a.bias != nullptr) {
+    float b[R];
+    load_row<float, V, R>(a.bias, a.experts, lane, b);
+#pragma unroll
+    for (int r = 0; r < R; ++r) c[r] += b[r];
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) key[r] = ordered(c[r]);
+  if (!(finite && whole)) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (!(x[r] > -INFINITY) || c[r] != c[r]) key[r] = 0u;
+  }
+  int my_id = -1;
 
   if (a.groups > 1) {
     uint32_t* keys = smem_keys + warp * a.experts;
@@ -338,19 +378,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
     if ((stay >> lane) & 1u) group_list[warp][__popc(stay & ((1u << lane) - 1u))] = lane;
     __syncwarp();
     const int n = __popc(stay) * size;
-    used = (n + 31) / 32;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (r >= used) break;
-      const int c = r * 32 + lane, g = c / size;
-      key[r] = 0u;
-      if (c < n) {
-        expert[r] = group_list[warp][g] * size + (c - g * size);
-        key[r] = keys[expert[r]];
-      }
+    if (n <= 8 * R) {
+      my_id = choose_of<R / 4>(keys, group_list[warp], size, n, a.k, lane, lists[warp]);
+    } else {
+      my_id = choose_of<R>(keys, group_list[warp], size, n, a.k, lane, lists[warp]);
     }
+  } else {
+    my_id = choose<R>(key, expert, a.k, lane, lists[warp]);
   }
-  const int my_id = choose<R>(key, expert, used, a.k, lane, lists[warp]);
 
   // Lane j holds the j-th choice; its logit is in L1.
   float s = 0.f;
