@@ -9,6 +9,7 @@ the shared library is missing or the device is not sm_103, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence, Tuple, Union
 
@@ -414,32 +415,60 @@ def muon_adamw_step(handle: int, params: Sequence, grads: Sequence, exp_avg: Seq
 
 
 # ------------------------------------------------ mixture-of-experts layer
-_DTYPES = {"torch.float32": 0, "torch.bfloat16": 1}
+class _Kinds(dict):
+    """Sets of PyTorch dtypes by name, made when first asked for (the package
+    imports without PyTorch)."""
+
+    def __missing__(self, kind):
+        import torch
+        names = {"f32": ("float32",), "bf16": ("bfloat16",), "f32/bf16": ("float32", "bfloat16"),
+                 "i32": ("int32",), "e4m3": ("float8_e4m3fn", "uint8"),
+                 "e8m0": ("uint8", "float8_e8m0fnu"), "bytes": ("uint8", "bool")}[kind]
+        self[kind] = out = frozenset(getattr(torch, n) for n in names if hasattr(torch, n))
+        return out
+
+
+_KINDS = _Kinds()
+
+
+def _want(name: str, t, shape: tuple, kind: str) -> int:
+    """Address of a contiguous CUDA tensor of this shape and kind."""
+    if t.dtype in _KINDS[kind] and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype not in _KINDS[kind]:
+        raise ValueError(f"{name} must be {' or '.join(map(str, _KINDS[kind]))}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _dtype(t) -> int:
-    """muon_dtype_t of a tensor."""
-    d = _DTYPES.get(str(t.dtype))
-    if d is None:
-        raise ValueError(f"expected an FP32 or BF16 tensor, got {t.dtype}")
-    return d
+    """muon_dtype_t of an FP32 or BF16 tensor."""
+    return 0 if t.dtype in _KINDS["f32"] else 1
 
 
-def _want(name: str, t, shape, dtypes) -> int:
-    """Address of a contiguous CUDA tensor of this shape and type."""
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if str(t.dtype).removeprefix("torch.") not in dtypes:
-        raise ValueError(f"{name} must be {' or '.join(dtypes)}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return _ptr(t)
+_raw_stream = None
 
 
-_F32, _BF16, _I32 = ("float32",), ("bfloat16",), ("int32",)
-_F8 = ("float8_e4m3fn", "uint8")
-_E8 = ("uint8", "float8_e8m0fnu")
-_BYTES = ("uint8", "bool")
+def _stream_of(stream, t) -> int:
+    """The given stream, or the current one of the tensor's device."""
+    global _raw_stream
+    if stream is not None:
+        return _stream(stream)
+    if _raw_stream is None:
+        import torch
+        # The raw handle, without making a Stream object for every call.
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(t.get_device())
+
+
+@functools.lru_cache(maxsize=64)
+def _route_options(*fields):
+    opts = _RouteOptions(*fields)
+    return opts, ctypes.byref(opts)
 
 
 def _nb(n: int) -> int:
@@ -455,13 +484,13 @@ def muon_moe_route(handle: int, logits, ids, weights, score: int = SCORE_SIGMOID
     tokens off."""
     t, e = logits.shape
     k = ids.shape[-1]
-    opts = _RouteOptions(score, groups, top_groups, group_top, 1 if renormalize else 0, scale)
+    _, opts = _route_options(score, groups, top_groups, group_top, 1 if renormalize else 0, scale)
     _check(load_library().muon_moe_route(
-        handle, t, e, k, _want("logits", logits, (t, e), _F32 + _BF16), _dtype(logits),
-        0 if bias is None else _want("bias", bias, (e,), _F32),
-        0 if mask is None else _want("mask", mask, (t,), _BYTES), ctypes.byref(opts),
-        _want("ids", ids, (t, k), _I32), _want("weights", weights, (t, k), _F32),
-        _stream(stream)))
+        handle, t, e, k, _want("logits", logits, (t, e), "f32/bf16"), _dtype(logits),
+        0 if bias is None else _want("bias", bias, (e,), "f32"),
+        0 if mask is None else _want("mask", mask, (t,), "bytes"), opts,
+        _want("ids", ids, (t, k), "i32"), _want("weights", weights, (t, k), "f32"),
+        _stream_of(stream, logits)))
 
 
 def muon_moe_route_backward(handle: int, logits, ids, grad_weights, grad_logits,
@@ -470,13 +499,14 @@ def muon_moe_route_backward(handle: int, logits, ids, grad_weights, grad_logits,
     """Gradient of the logits (written whole, the logits' type)."""
     t, e = logits.shape
     k = ids.shape[-1]
-    opts = _RouteOptions(score, 1, 1, 1, 1 if renormalize else 0, scale)
+    kind = _dtype(logits)
+    _, opts = _route_options(score, 1, 1, 1, 1 if renormalize else 0, scale)
     _check(load_library().muon_moe_route_backward(
-        handle, t, e, k, _want("logits", logits, (t, e), _F32 + _BF16), _dtype(logits),
-        _want("ids", ids, (t, k), _I32), _want("grad_weights", grad_weights, (t, k), _F32),
-        ctypes.byref(opts),
-        _want("grad_logits", grad_logits, (t, e), (str(logits.dtype).removeprefix("torch."),)),
-        _stream(stream)))
+        handle, t, e, k, _want("logits", logits, (t, e), "f32/bf16"), _dtype(logits),
+        _want("ids", ids, (t, k), "i32"), _want("grad_weights", grad_weights, (t, k), "f32"),
+        opts,
+        _want("grad_logits", grad_logits, (t, e), "f32" if kind == 0 else "bf16"),
+        _stream_of(stream, logits)))
 
 
 def muon_moe_plan(handle: int, ids, offsets, slots, pos, stream=None) -> None:
@@ -486,17 +516,17 @@ def muon_moe_plan(handle: int, ids, offsets, slots, pos, stream=None) -> None:
     n = ids.numel()
     e = offsets.shape[0] - 1
     _check(load_library().muon_moe_plan(
-        handle, n, e, _want("ids", ids, ids.shape, _I32), _want("offsets", offsets, (e + 1,), _I32),
-        _want("slots", slots, (n,), _I32), _want("pos", pos, ids.shape, _I32), _stream(stream)))
+        handle, n, e, _want("ids", ids, ids.shape, "i32"), _want("offsets", offsets, (e + 1,), "i32"),
+        _want("slots", slots, (n,), "i32"), _want("pos", pos, ids.shape, "i32"), _stream_of(stream, ids)))
 
 
 def muon_moe_combine(handle: int, y, pos, weights, out, stream=None) -> None:
     """out[t] = sum over j of weights[t, j] y[pos[t, j]]; weights None: ones."""
     (r, d), (t, k) = y.shape, pos.shape
     _check(load_library().muon_moe_combine(
-        handle, t, k, r, d, _want("y", y, (r, d), _BF16), _want("pos", pos, (t, k), _I32),
-        0 if weights is None else _want("weights", weights, (t, k), _F32),
-        _want("out", out, (t, d), _BF16), _stream(stream)))
+        handle, t, k, r, d, _want("y", y, (r, d), "bf16"), _want("pos", pos, (t, k), "i32"),
+        0 if weights is None else _want("weights", weights, (t, k), "f32"),
+        _want("out", out, (t, d), "bf16"), _stream_of(stream, y)))
 
 
 def muon_moe_combine_backward(handle: int, grad_out, y, pos, weights, grad_y, grad_weights=None,
@@ -505,12 +535,12 @@ def muon_moe_combine_backward(handle: int, grad_out, y, pos, weights, grad_y, gr
     be None too."""
     (r, d), (t, k) = grad_y.shape, pos.shape
     _check(load_library().muon_moe_combine_backward(
-        handle, t, k, r, d, _want("grad_out", grad_out, (t, d), _BF16),
-        0 if y is None else _want("y", y, (r, d), _BF16), _want("pos", pos, (t, k), _I32),
-        0 if weights is None else _want("weights", weights, (t, k), _F32),
-        _want("grad_y", grad_y, (r, d), _BF16),
-        0 if grad_weights is None else _want("grad_weights", grad_weights, (t, k), _F32),
-        _stream(stream)))
+        handle, t, k, r, d, _want("grad_out", grad_out, (t, d), "bf16"),
+        0 if y is None else _want("y", y, (r, d), "bf16"), _want("pos", pos, (t, k), "i32"),
+        0 if weights is None else _want("weights", weights, (t, k), "f32"),
+        _want("grad_y", grad_y, (r, d), "bf16"),
+        0 if grad_weights is None else _want("grad_weights", grad_weights, (t, k), "f32"),
+        _stream_of(stream, grad_out)))
 
 
 def muon_fp8_quantize_rows(handle: int, x, q, scales, pos=None, stream=None) -> None:
@@ -523,9 +553,9 @@ def muon_fp8_quantize_rows(handle: int, x, q, scales, pos=None, stream=None) -> 
     elif r != t:
         raise ValueError(f"q must have {t} rows, got {r}")
     _check(load_library().muon_fp8_quantize_rows(
-        handle, t, d, _want("x", x, (t, d), _BF16),
-        0 if pos is None else _want("pos", pos, (t, k), _I32), k, r, _want("q", q, (r, d), _F8),
-        _want("scales", scales, (r, _nb(d)), _E8), _stream(stream)))
+        handle, t, d, _want("x", x, (t, d), "bf16"),
+        0 if pos is None else _want("pos", pos, (t, k), "i32"), k, r, _want("q", q, (r, d), "e4m3"),
+        _want("scales", scales, (r, _nb(d)), "e8m0"), _stream_of(stream, x)))
 
 
 def muon_fp8_quantize_blocks(handle: int, w, q=None, scales=None, qt=None, scales_t=None,
@@ -535,12 +565,12 @@ def muon_fp8_quantize_blocks(handle: int, w, q=None, scales=None, qt=None, scale
     (``qt``, ``scales_t``)."""
     e, n, k = w.shape
     _check(load_library().muon_fp8_quantize_blocks(
-        handle, e, n, k, _want("w", w, (e, n, k), _F32 + _BF16), _dtype(w),
-        0 if q is None else _want("q", q, (e, n, k), _F8),
-        0 if scales is None else _want("scales", scales, (e, _nb(n), _nb(k)), _E8),
-        0 if qt is None else _want("qt", qt, (e, k, n), _F8),
-        0 if scales_t is None else _want("scales_t", scales_t, (e, _nb(k), _nb(n)), _E8),
-        _stream(stream)))
+        handle, e, n, k, _want("w", w, (e, n, k), "f32/bf16"), _dtype(w),
+        0 if q is None else _want("q", q, (e, n, k), "e4m3"),
+        0 if scales is None else _want("scales", scales, (e, _nb(n), _nb(k)), "e8m0"),
+        0 if qt is None else _want("qt", qt, (e, k, n), "e4m3"),
+        0 if scales_t is None else _want("scales_t", scales_t, (e, _nb(k), _nb(n)), "e8m0"),
+        _stream_of(stream, w)))
 
 
 def muon_fp8_cols_capacity(rows: int, experts: int) -> int:
@@ -557,10 +587,10 @@ def muon_fp8_quantize_cols(handle: int, x, offsets, qt, scales, slots=None, top_
     (xr, d), e, cap = x.shape, offsets.shape[0] - 1, qt.shape[1]
     rows = xr if slots is None else slots.shape[0]
     _check(load_library().muon_fp8_quantize_cols(
-        handle, xr, d, _want("x", x, (xr, d), _BF16), e, _want("offsets", offsets, (e + 1,), _I32),
-        rows, 0 if slots is None else _want("slots", slots, (rows,), _I32), top_k,
-        _want("qt", qt, (d, cap), _F8), cap, _want("scales", scales, (cap // 128, d), _E8),
-        _stream(stream)))
+        handle, xr, d, _want("x", x, (xr, d), "bf16"), e, _want("offsets", offsets, (e + 1,), "i32"),
+        rows, 0 if slots is None else _want("slots", slots, (rows,), "i32"), top_k,
+        _want("qt", qt, (d, cap), "e4m3"), cap, _want("scales", scales, (cap // 128, d), "e8m0"),
+        _stream_of(stream, x)))
 
 
 def muon_fp8_grouped_matmul(handle: int, x, x_scales, w, w_scales, offsets, y,
@@ -569,10 +599,10 @@ def muon_fp8_grouped_matmul(handle: int, x, x_scales, w, w_scales, offsets, y,
     expert; ``x`` [rows, k], ``w`` [experts, n, k] e4m3, ``y`` [rows, n] BF16."""
     (r, k), (e, n, _) = x.shape, w.shape
     _check(load_library().muon_fp8_grouped_matmul(
-        handle, r, e, n, k, _want("x", x, (r, k), _F8),
-        _want("x_scales", x_scales, (r, _nb(k)), _E8), _want("w", w, (e, n, k), _F8),
-        _want("w_scales", w_scales, (e, _nb(n), _nb(k)), _E8),
-        _want("offsets", offsets, (e + 1,), _I32), _want("y", y, (r, n), _BF16), _stream(stream)))
+        handle, r, e, n, k, _want("x", x, (r, k), "e4m3"),
+        _want("x_scales", x_scales, (r, _nb(k)), "e8m0"), _want("w", w, (e, n, k), "e4m3"),
+        _want("w_scales", w_scales, (e, _nb(n), _nb(k)), "e8m0"),
+        _want("offsets", offsets, (e + 1,), "i32"), _want("y", y, (r, n), "bf16"), _stream_of(stream, x)))
 
 
 def muon_fp8_grouped_wgrad(handle: int, yt, yt_scales, xt, xt_scales, offsets, dw,
@@ -582,11 +612,11 @@ def muon_fp8_grouped_wgrad(handle: int, yt, yt_scales, xt, xt_scales, offsets, d
     FP32."""
     (n, cap), k, e = yt.shape, xt.shape[0], offsets.shape[0] - 1
     _check(load_library().muon_fp8_grouped_wgrad(
-        handle, e, n, k, cap, _want("yt", yt, (n, cap), _F8),
-        _want("yt_scales", yt_scales, (cap // 128, n), _E8), _want("xt", xt, (k, cap), _F8),
-        _want("xt_scales", xt_scales, (cap // 128, k), _E8),
-        _want("offsets", offsets, (e + 1,), _I32), _want("dw", dw, (e, n, k), _F32),
-        1 if accumulate else 0, _stream(stream)))
+        handle, e, n, k, cap, _want("yt", yt, (n, cap), "e4m3"),
+        _want("yt_scales", yt_scales, (cap // 128, n), "e8m0"), _want("xt", xt, (k, cap), "e4m3"),
+        _want("xt_scales", xt_scales, (cap // 128, k), "e8m0"),
+        _want("offsets", offsets, (e + 1,), "i32"), _want("dw", dw, (e, n, k), "f32"),
+        1 if accumulate else 0, _stream_of(stream, yt)))
 
 
 def muon_selftest_bounded_wait(handle: int, limit_ms: int = 50, stream=None) -> None:
