@@ -227,16 +227,31 @@ __global__ void __launch_bounds__(kTileThreads) quantize_blocks_kernel(
 }
 
 // ------------------------------------------------------------------ columns
-// Persistent blocks over (128-column stripe, block of 128 rows of one expert),
-// the row blocks of a stripe one after the other: a stripe of the gathered x
-// (tokens x 256 bytes) is read from HBM once and from L2 for the token's
-// other experts.
-__global__ void __launch_bounds__(kTileThreads) quantize_cols_kernel(
+// Persistent blocks over (chunk of kStripes 128-column stripes, block of 128
+// rows of one expert), all row blocks of a chunk before the next chunk's: the
+// gathered rows of a chunk (tokens x 1 KB) stay in L2 while the token's other
+// experts read them, and a row block looks up its rows once per chunk.  The next
+// stripe's loads are in flight while a stripe is written.
+// Magnitudes are compared as pairs of 16-bit integers and scaled as BF16 pairs
+// (exact: a power of two; what underflows BF16 is far below e4m3's least), which
+// halves the instructions: without that the kernel is bound by them.
+constexpr int kStripes = 4;
+
+// Two scaled BF16 values as e4m3 bytes.
+__device__ __forceinline__ uint32_t pair_to_e4m3(uint32_t u, uint32_t inv) {
+  const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&u);
+  const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&inv);
+  const __nv_bfloat162 v = __hmul2(a, b);
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&v);
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo(w), hi(w)), __NV_SATFINITE, __NV_E4M3);
+}
+
+__global__ void __launch_bounds__(kTileThreads, 3) quantize_cols_kernel(
     const uint16_t* __restrict__ x, int64_t x_rows, int d, const int32_t* __restrict__ offsets,
     int experts, const int32_t* __restrict__ slots, int top_k, int64_t rows,
     uint8_t* __restrict__ qt, int64_t cap, uint8_t* __restrict__ scales, int* err) {
   __shared__ __align__(16) uint8_t tile[128 * 128];
-  __shared__ uint32_t col_max[kTileThreads / 32][128];
+  __shared__ uint2 col_max[kTileThreads / 32][32];
   __shared__ int32_t first[kMoeMaxExperts + 1];   // first row block of each expert
   __shared__ int32_t warp_total[kTileThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -275,11 +290,11 @@ __global__ void __launch_bounds__(kTileThreads) quantize_cols_kernel(
     blocks = static_cast<int>(cap / 128);
   }
   const int stripes = (d + 127) / 128;
-  const int64_t tiles = static_cast<int64_t>(stripes) * blocks;
+  const int64_t units = static_cast<int64_t>((stripes + kStripes - 1) / kStripes) * blocks;
 
-  for (int64_t tid = blockIdx.x; tid < tiles; tid += gridDim.x) {
-    const int stripe = static_cast<int>(tid / blocks);
-    const int b = static_cast<int>(tid - static_cast<int64_t>(stripe) * blocks);
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int chunk = static_cast<int>(unit / blocks);
+    const int b = static_cast<int>(unit - static_cast<int64_t>(chunk) * blocks);
     // The expert of row block b: the last one that starts at or before it.
     int lo_e = 0, hi_e = experts;
     while (hi_e - lo_e > 1) {
@@ -288,69 +303,99 @@ __global__ void __launch_bounds__(kTileThreads) quantize_cols_kernel(
     }
     const int64_t row_end = offsets[lo_e + 1];
     const int64_t row0 = offsets[lo_e] + static_cast<int64_t>(b - first[lo_e]) * 128 + warp * 16;
-    const int c0 = stripe * 128, col = c0 + lane * 4;
 
-    // Lane r of the warp looks up row r's source once.
-    int64_t src = -1;
+    // Lane r of the warp looks up row r's source.
+    int src = -1;
     if (lane < 16 && row0 + lane < row_end) {
-      src = row0 + lane;
-      if (src < 0 || src >= rows) {
-        src = -1;
-      } else if (slots != nullptr) {
-        const int slot = slots[src];
-        src = slot >= 0 ? slot / top_k : -1;
+      const int64_t r = row0 + lane;
+      if (r >= 0 && r < rows) {
+        src = static_cast<int>(r);
+        if (slots != nullptr) {
+          const int slot = slots[r];
+          src = slot >= 0 ? slot / top_k : -1;
+        }
       }
       if (src < 0 || src >= x_rows) {
         atomicOr(err, kDevErrIndex);
         src = -1;
       }
     }
+    const bool any = __any_sync(kAll, src >= 0);  // some row of this warp is there
+    const int stripe0 = chunk * kStripes, stripe1 = min(stripes, stripe0 + kStripes);
     uint2 u[16];
+    const auto load = [&](int stripe) {
+      const int col = stripe * 128 + lane * 4;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int64_t from = __shfl_sync(kAll, src, r);
-      u[r] = from >= 0 && col < d ? *reinterpret_cast<const uint2*>(x + from * d + col)
-                                  : make_uint2(0u, 0u);
-    }
-    bool bad = false;
-    uint32_t m[4] = {0u, 0u, 0u, 0u};
+      for (int r = 0; r < 16; ++r) {
+        const int from = __shfl_sync(kAll, src, r);
+        u[r] = make_uint2(0u, 0u);
+        if (from >= 0 && col < d)
+          u[r] = __ldg(reinterpret_cast<const uint2*>(x + static_cast<int64_t>(from) * d + col));
+      }
+    };
+    if (any) load(stripe0);
+    for (int stripe = stripe0; stripe < stripe1; ++stripe) {
+      const int c0 = stripe * 128, col = c0 + lane * 4;
+      uint2 m = make_uint2(0u, 0u);
+      if (any) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      m[0] = max(m[0], mag(lo(u[r].x), bad));
-      m[1] = max(m[1], mag(hi(u[r].x), bad));
-      m[2] = max(m[2], mag(lo(u[r].y), bad));
-      m[3] = max(m[3], mag(hi(u[r].y), bad));
-    }
-    if (bad) atomicOr(err, kDevErrInput);
-    *reinterpret_cast<uint4*>(&col_max[warp][lane * 4]) = make_uint4(m[0], m[1], m[2], m[3]);
-    __syncthreads();
-    float inv[4];
-    int ex[4];
+        for (int r = 0; r < 16; ++r) {
+          m.x = __vmaxu2(m.x, u[r].x & 0x7fff7fffu);
+          m.y = __vmaxu2(m.y, u[r].y & 0x7fff7fffu);
+        }
+      }
+      col_max[warp][lane] = m;
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kTileThreads / 32; ++w) {
-      const uint4 o = *reinterpret_cast<const uint4*>(&col_max[w][lane * 4]);
-      m[0] = max(m[0], o.x); m[1] = max(m[1], o.y); m[2] = max(m[2], o.z); m[3] = max(m[3], o.w);
-    }
+      for (int w = 0; w < kTileThreads / 32; ++w) {
+        const uint2 o = col_max[w][lane];
+        m.x = __vmaxu2(m.x, o.x);
+        m.y = __vmaxu2(m.y, o.y);
+      }
+      uint32_t top[4] = {m.x << 16, m.x & 0xffff0000u, m.y << 16, m.y & 0xffff0000u};
+      if (max(max(top[0], top[1]), max(top[2], top[3])) >= kInfBits) {
+        atomicOr(err, kDevErrInput);
+        // NaN takes no part in the magnitude: this warp's columns again, over
+        // all rows of the block.
+        for (int c = 0; c < 4; ++c) {
+          if (top[c] <= kInfBits) continue;
+          top[c] = 0u;
+          const int64_t r_begin = row0 - warp * 16, r_end = min(row_end, r_begin + 128);
+          for (int64_t r = max(r_begin, int64_t(0)); r < min(r_end, rows); ++r) {
+            int64_t from = r;
+            if (slots != nullptr) from = slots[r] >= 0 ? slots[r] / top_k : -1;
+            if (from < 0 || from >= x_rows || col >= d) continue;
+            const uint32_t v = static_cast<uint32_t>(x[from * d + col + c] & 0x7fffu) << 16;
+            if (v <= kInfBits) top[c] = max(top[c], v);
+          }
+        }
+      }
+      int ex[4];
+      uint32_t inv[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      ex[c] = scale_exponent(m[c]);
-      inv[c] = inverse_scale(ex[c]);
-    }
-    uint32_t words[16];
+      for (int c = 0; c < 4; ++c) {
+        ex[c] = scale_exponent(top[c]);
+        inv[c] = static_cast<uint32_t>(127 - ex[c]) << 7;          // 2^-ex as BF16 bits
+      }
+      const uint32_t inv01 = inv[0] | (inv[1] << 16), inv23 = inv[2] | (inv[3] << 16);
+      uint32_t words[16];
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-      words[r] = to_e4m3x4(lo(u[r].x) * inv[0], hi(u[r].x) * inv[1], lo(u[r].y) * inv[2],
-                           hi(u[r].y) * inv[3], 1.0f);
-    put_transposed(tile, words, warp, lane);
-    if (warp == 0 && col < d) {
-      const uint32_t bytes = static_cast<uint32_t>(ex[0] + 127) | (static_cast<uint32_t>(ex[1] + 127) << 8) |
-                             (static_cast<uint32_t>(ex[2] + 127) << 16) | (static_cast<uint32_t>(ex[3] + 127) << 24);
-      *reinterpret_cast<uint32_t*>(scales + static_cast<int64_t>(b) * d + col) = bytes;
+      for (int r = 0; r < 16; ++r)
+        words[r] = any ? pair_to_e4m3(u[r].x, inv01) | (pair_to_e4m3(u[r].y, inv23) << 16) : 0u;
+      if (any && stripe + 1 < stripe1) load(stripe + 1);
+      put_transposed(tile, words, warp, lane);
+      if (warp == 0 && col < d) {
+        const uint32_t bytes = static_cast<uint32_t>(ex[0] + 127) | (static_cast<uint32_t>(ex[1] + 127) << 8) |
+                               (static_cast<uint32_t>(ex[2] + 127) << 16) | (static_cast<uint32_t>(ex[3] + 127) << 24);
+        *reinterpret_cast<uint32_t*>(scales + static_cast<int64_t>(b) * d + col) = bytes;
+      }
+      __syncthreads();
+      write_transposed(tile, qt + static_cast<int64_t>(c0) * cap + static_cast<int64_t>(b) * 128, cap,
+                       min(128, d - c0), 128);
+      // No barrier here: the next stripe's writes to `tile` come after the
+      // barrier that follows col_max, which every thread reaches after its
+      // reads of `tile`; col_max was read before this stripe's second one.
     }
-    __syncthreads();
-    write_transposed(tile, qt + static_cast<int64_t>(c0) * cap + static_cast<int64_t>(b) * 128, cap,
-                     min(128, d - c0), 128);
-    __syncthreads();                              // tile and col_max are free again
   }
 }
 
@@ -380,7 +425,7 @@ cudaError_t launch_fp8_quantize_cols(const uint16_t* x, int64_t x_rows, int d,
                                      int top_k, int64_t rows, uint8_t* qt, int64_t cap,
                                      uint8_t* scales, int* err, int num_sms, cudaStream_t s) {
   const int64_t tiles = (cap / 128) * ((d + 127) / 128);
-  const int64_t grid = tiles < 4 * num_sms ? tiles : 4 * num_sms;
+  const int64_t grid = tiles < 3 * num_sms ? tiles : 3 * num_sms;   // three blocks per SM
   return launch_pdl(quantize_cols_kernel, dim3(static_cast<unsigned>(grid)), dim3(kTileThreads), 0, s,
                     x, x_rows, d, offsets, experts, slots, top_k, rows, qt, cap, scales, err);
 }
