@@ -35,13 +35,12 @@ constexpr uint32_t kAll = 0xffffffffu;
 constexpr uint32_t kInfBits = 0x7f800000u;
 
 // Exponent e of the scale of a block whose largest magnitude has these FP32
-// bits (an infinity: the largest finite exponent's).
+// bits (an infinity: the largest finite exponent's).  The addend carries into
+// the exponent field when the fraction is above 1.75's; below 2^-127 of a scale
+// there is none, and 2^-127 serves.
 __device__ __forceinline__ int scale_exponent(uint32_t bits) {
-  if (bits == 0u) return 0;
-  const int p = static_cast<int>(bits >> 23) - 127;
-  if (p == 128) return 120;
-  if (p == -127) return -127;             // subnormal: 2^-127 serves all of them
-  return max(-127, p - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0));
+  const int e = static_cast<int>((bits + 0x1fffffu) >> 23) - 135;
+  return bits == 0u ? 0 : max(-127, e);
 }
 
 // 2^-e as FP32, -127 <= e <= 120.
@@ -56,13 +55,42 @@ __device__ __forceinline__ uint32_t mag(float v, bool& bad) {
   return u > kInfBits ? 0u : u;
 }
 
-// Four values times `inv` as e4m3 bytes, saturating.
-__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d, float inv) {
-  const __nv_fp8x2_storage_t p =
-      __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3);
-  const __nv_fp8x2_storage_t q =
-      __nv_cvt_float2_to_fp8x2(make_float2(c * inv, d * inv), __NV_SATFINITE, __NV_E4M3);
-  return static_cast<uint32_t>(p) | (static_cast<uint32_t>(q) << 16);
+// Two values times `inv` as e4m3 bytes, saturating.
+__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b, float inv) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Two pairs of BF16 values times two pairs of scales as four bytes: mixed-
+// precision FMAs (the addend -0 keeps a zero's sign) take the halves as they
+// lie.
+__device__ __forceinline__ uint32_t bf16_to_e4m3x4(uint32_t u, uint32_t v, uint32_t inv_u,
+                                                   uint32_t inv_v) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b, c, d, p, q;\n\t.reg .f32 f, g;\n\t"
+      "mov.b32 {a, b}, %1;\n\t"
+      "mov.b32 {c, d}, %3;\n\t"
+      "fma.rn.f32.bf16 f, a, c, 0f80000000;\n\t"
+      "fma.rn.f32.bf16 g, b, d, 0f80000000;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 p, g, f;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "mov.b32 {c, d}, %4;\n\t"
+      "fma.rn.f32.bf16 f, a, c, 0f80000000;\n\t"
+      "fma.rn.f32.bf16 g, b, d, 0f80000000;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 q, g, f;\n\t"
+      "mov.b32 %0, {p, q};\n\t}"
+      : "=r"(r)
+      : "r"(u), "r"(v), "r"(inv_u), "r"(inv_v));
+  return r;
+}
+
+// Largest magnitude bits of BF16 pairs, as 16-bit integers (NaN the largest).
+__device__ __forceinline__ uint32_t max_mag2(uint32_t m, uint32_t u) {
+  return __vmaxu2(m, u & 0x7fff7fffu);
+}
+
+// 2^-e as BF16 bits.
+__device__ __forceinline__ uint32_t inverse_scale_bf16(int e) {
+  return static_cast<uint32_t>(127 - e) << 7;
 }
 
 __device__ __forceinline__ float lo(uint32_t u) { return __uint_as_float(u << 16); }
@@ -87,19 +115,25 @@ __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(
   const bool in = live && c < d;
   uint4 u = make_uint4(0, 0, 0, 0);
   if (in) u = *reinterpret_cast<const uint4*>(x + t * d + c);
-  const float v[8] = {lo(u.x), hi(u.x), lo(u.y), hi(u.y), lo(u.z), hi(u.z), lo(u.w), hi(u.w)};
-  bool bad = false;
-  uint32_t m = 0u;
+  uint32_t m2 = max_mag2(max_mag2(max_mag2(u.x & 0x7fff7fffu, u.y), u.z), u.w);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, mag(v[i], bad));
+  for (int o = 8; o > 0; o >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(kAll, m2, o));
+  uint32_t m = max(m2 & 0xffff0000u, m2 << 16);
+  if (__any_sync(kAll, m >= kInfBits)) {          // NaN takes no part in the magnitude
+    const float v[8] = {lo(u.x), hi(u.x), lo(u.y), hi(u.y), lo(u.z), hi(u.z), lo(u.w), hi(u.w)};
+    bool bad = false;
+    m = 0u;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
-  if (bad) atomicOr(err, kDevErrInput);
+    for (int i = 0; i < 8; ++i) m = max(m, mag(v[i], bad));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
+    if (bad) atomicOr(err, kDevErrInput);
+  }
   if (!live) return;
   const int e = scale_exponent(m);
-  const float inv = inverse_scale(e);
-  const uint2 out = make_uint2(to_e4m3x4(v[0], v[1], v[2], v[3], inv),
-                               to_e4m3x4(v[4], v[5], v[6], v[7], inv));
+  const uint32_t inv = inverse_scale_bf16(e) * 0x10001u;
+  const uint2 out =
+      make_uint2(bf16_to_e4m3x4(u.x, u.y, inv, inv), bf16_to_e4m3x4(u.z, u.w, inv, inv));
   if (pos == nullptr) {
     if (in) *reinterpret_cast<uint2*>(q + t * d + c) = out;
     if (sub == 0) scales[t * blocks + b] = static_cast<uint8_t>(e + 127);
@@ -129,22 +163,25 @@ __device__ __forceinline__ uint32_t tile_chunk(int col, int chunk) {
   return static_cast<uint32_t>(col * 128 + ((chunk ^ ((col >> 2) & 7)) << 4));
 }
 
-// words[r] holds row r's four bytes of this thread; stores its 16 x 4 piece.
+// words[r] holds row r's four bytes of this thread; stores its 16 x 4 piece:
+// 4 x 4 byte transposes.
 __device__ __forceinline__ void put_transposed(uint8_t* tile, const uint32_t (&words)[16], int warp,
                                                int lane) {
+  uint32_t out[4][4];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t out[4];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      // Byte c of four rows: a 4 x 4 byte transpose, one column at a time.
-      const uint32_t ab = __byte_perm(words[4 * g], words[4 * g + 1], 0x0040u + c * 0x0011u);
-      const uint32_t cd = __byte_perm(words[4 * g + 2], words[4 * g + 3], 0x0040u + c * 0x0011u);
-      out[g] = __byte_perm(ab, cd, 0x5410u);
-    }
-    *reinterpret_cast<uint4*>(tile + tile_chunk(lane * 4 + c, warp)) =
-        make_uint4(out[0], out[1], out[2], out[3]);
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t a = words[4 * g], b = words[4 * g + 1], c = words[4 * g + 2], d = words[4 * g + 3];
+    const uint32_t ab = __byte_perm(a, b, 0x5140), cd = __byte_perm(c, d, 0x5140);
+    const uint32_t ef = __byte_perm(a, b, 0x7362), gh = __byte_perm(c, d, 0x7362);
+    out[0][g] = __byte_perm(ab, cd, 0x5410);
+    out[1][g] = __byte_perm(ab, cd, 0x7632);
+    out[2][g] = __byte_perm(ef, gh, 0x5410);
+    out[3][g] = __byte_perm(ef, gh, 0x7632);
   }
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4*>(tile + tile_chunk(lane * 4 + c, warp)) =
+        make_uint4(out[c][0], out[c][1], out[c][2], out[c][3]);
 }
 
 // Rows (the source's columns) of the transposed tile to dst, `width` bytes
@@ -209,7 +246,8 @@ __global__ void __launch_bounds__(kTileThreads) quantize_blocks_kernel(
   const float inv = inverse_scale(e);
   uint32_t words[16];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) words[r] = to_e4m3x4(v[r].x, v[r].y, v[r].z, v[r].w, inv);
+  for (int r = 0; r < 16; ++r)
+    words[r] = to_e4m3x2(v[r].x, v[r].y, inv) | (to_e4m3x2(v[r].z, v[r].w, inv) << 16);
   if (q != nullptr) {
 #pragma unroll
     for (int r = 0; r < 16; ++r)
@@ -232,19 +270,10 @@ __global__ void __launch_bounds__(kTileThreads) quantize_blocks_kernel(
 // gathered rows of a chunk (tokens x 1 KB) stay in L2 while the token's other
 // experts read them, and a row block looks up its rows once per chunk.  The next
 // stripe's loads are in flight while a stripe is written.
-// Magnitudes are compared as pairs of 16-bit integers and scaled as BF16 pairs
-// (exact: a power of two; what underflows BF16 is far below e4m3's least), which
-// halves the instructions: without that the kernel is bound by them.
+// Magnitudes are compared as pairs of 16-bit integers and values scaled by
+// mixed-precision FMAs that take BF16 halves in place: the kernel is bound by
+// its instructions, not by memory.
 constexpr int kStripes = 4;
-
-// Two scaled BF16 values as e4m3 bytes.
-__device__ __forceinline__ uint32_t pair_to_e4m3(uint32_t u, uint32_t inv) {
-  const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&u);
-  const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&inv);
-  const __nv_bfloat162 v = __hmul2(a, b);
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(&v);
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo(w), hi(w)), __NV_SATFINITE, __NV_E4M3);
-}
 
 __global__ void __launch_bounds__(kTileThreads, 3) quantize_cols_kernel(
     const uint16_t* __restrict__ x, int64_t x_rows, int d, const int32_t* __restrict__ offsets,
@@ -323,14 +352,26 @@ __global__ void __launch_bounds__(kTileThreads, 3) quantize_cols_kernel(
     const bool any = __any_sync(kAll, src >= 0);  // some row of this warp is there
     const int stripe0 = chunk * kStripes, stripe1 = min(stripes, stripe0 + kStripes);
     uint2 u[16];
+    const bool all = __all_sync(kAll, src >= 0 || lane >= 16);
+    // Row starts in units of 16 values: 32 bits reach 2^36 values.
+    const uint32_t row_at = static_cast<uint32_t>(max(src, 0)) * static_cast<uint32_t>(d >> 4);
     const auto load = [&](int stripe) {
       const int col = stripe * 128 + lane * 4;
+      const uint16_t* from = x + col;
+      if (all && stripe * 128 + 128 <= d) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int from = __shfl_sync(kAll, src, r);
-        u[r] = make_uint2(0u, 0u);
-        if (from >= 0 && col < d)
-          u[r] = __ldg(reinterpret_cast<const uint2*>(x + static_cast<int64_t>(from) * d + col));
+        for (int r = 0; r < 16; ++r)
+          u[r] = __ldg(reinterpret_cast<const uint2*>(
+              from + static_cast<uint64_t>(__shfl_sync(kAll, row_at, r)) * 16));
+      } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const uint32_t row = __shfl_sync(kAll, row_at, r);
+          const bool there = __shfl_sync(kAll, src, r) >= 0;
+          u[r] = make_uint2(0u, 0u);
+          if (there && col < d)
+            u[r] = __ldg(reinterpret_cast<const uint2*>(from + static_cast<uint64_t>(row) * 16));
+        }
       }
     };
     if (any) load(stripe0);
@@ -340,8 +381,8 @@ __global__ void __launch_bounds__(kTileThreads, 3) quantize_cols_kernel(
       if (any) {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          m.x = __vmaxu2(m.x, u[r].x & 0x7fff7fffu);
-          m.y = __vmaxu2(m.y, u[r].y & 0x7fff7fffu);
+          m.x = max_mag2(m.x, u[r].x);
+          m.y = max_mag2(m.y, u[r].y);
         }
       }
       col_max[warp][lane] = m;
@@ -375,13 +416,16 @@ __global__ void __launch_bounds__(kTileThreads, 3) quantize_cols_kernel(
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         ex[c] = scale_exponent(top[c]);
-        inv[c] = static_cast<uint32_t>(127 - ex[c]) << 7;          // 2^-ex as BF16 bits
+        inv[c] = inverse_scale_bf16(ex[c]);
       }
       const uint32_t inv01 = inv[0] | (inv[1] << 16), inv23 = inv[2] | (inv[3] << 16);
       uint32_t words[16];
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        words[r] = any ? pair_to_e4m3(u[r].x, inv01) | (pair_to_e4m3(u[r].y, inv23) << 16) : 0u;
+      for (int r = 0; r < 16; ++r) words[r] = 0u;
+      if (any) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) words[r] = bf16_to_e4m3x4(u[r].x, u[r].y, inv01, inv23);
+      }
       if (any && stripe + 1 < stripe1) load(stripe + 1);
       put_transposed(tile, words, warp, lane);
       if (warp == 0 && col < d) {

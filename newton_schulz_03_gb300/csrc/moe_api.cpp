@@ -335,6 +335,8 @@ muon_status_t muon_fp8_quantize_cols(muon_handle_t h, int64_t x_rows, int32_t hi
   MUON_TRY(check_rows(capacity));
   if (capacity % kFp8Block != 0)
     return fail(MUON_ERR_INVALID_ARG, "capacity must be a multiple of 128");
+  if (x_rows * (hidden / 16) >= (int64_t(1) << 32))
+    return fail(MUON_ERR_INVALID_ARG, "x is too large for one call");
   if (slots != nullptr && (top_k < 1 || top_k > muon::kMoeMaxTopK))
     return fail(MUON_ERR_INVALID_ARG, "top_k must be 1..%d (got %d)", muon::kMoeMaxTopK, top_k);
   if (rows == 0 || capacity == 0) return MUON_OK;
