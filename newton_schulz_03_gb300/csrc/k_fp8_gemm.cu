@@ -48,7 +48,6 @@ constexpr int kTileM = 256;                       // pair tile: output rows of w
 constexpr int kHalfM = 128;
 constexpr int kBK = 128;                          // K block: one 128-byte swizzle row, one scale
 constexpr int kABytes = kHalfM * kBK;             // 16 KB per CTA and stage
-constexpr int kStages = 6;
 constexpr int kSetBlocks = 4;                     // K blocks per set of scales
 constexpr int kSets = 4;                          // sets in the ring
 constexpr int kScaleBytes = 512 + 1024;           // per set: 128 A cells, 256 B cells
@@ -63,12 +62,14 @@ constexpr int kMaps = kMaxTokens / kWidthUnit;    // B boxes: half a width each
 template <bool GRAD>
 struct Layout {
   static constexpr int kAccCols = GRAD ? kGradN : kMaxTokens;
+  static constexpr int kStages = GRAD ? 4 : 6;                // operand stages
+  static constexpr int kOutBufs = GRAD ? 4 : 2;               // per epilogue warp
   static constexpr int kBBytes = (kAccCols / 2) * kBK;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kOutBuf = GRAD ? 4096 : 2048;          // one 32 x 32 chunk
   static constexpr int kScaleAt = kStages * kStageBytes;
   static constexpr int kOutAt = kScaleAt + kSets * kScaleBytes;
-  static constexpr int kTableAt = kOutAt + kEpiWarps * 2 * kOutBuf;
+  static constexpr int kTableAt = kOutAt + kEpiWarps * kOutBufs * kOutBuf;
   static constexpr int kTableBytes = (kMoeMaxExperts + 4) * 4;
   static constexpr int kBarAt = kTableAt + 2 * kTableBytes;
   static constexpr int kSmem = kBarAt + 256 + 1024;
@@ -110,23 +111,24 @@ struct Tile {
 // start[e]: its first row.
 template <bool GRAD>
 __device__ __forceinline__ bool decode(const Fp8Args& p, const int32_t* first, const int32_t* start,
-                                       int64_t t, Tile& o) {
+                                       uint32_t t, Tile& o) {
+  const uint32_t tiles_m = p.tiles_m;
   if (GRAD) {
-    const int per = p.tiles_m * p.tiles_n;
+    const uint32_t per = tiles_m * p.tiles_n;
     o.expert = static_cast<int>(t / per);
     if (o.expert >= p.experts) return false;
-    const int l = static_cast<int>(t - static_cast<int64_t>(o.expert) * per);
-    const int tn = l / p.tiles_m;
-    o.n0 = (l - tn * p.tiles_m) * kTileM;
-    o.c0 = tn * kGradN;
+    const uint32_t l = t - o.expert * per;
+    const uint32_t tn = l / tiles_m;
+    o.n0 = static_cast<int>(l - tn * tiles_m) * kTileM;
+    o.c0 = static_cast<int>(tn) * kGradN;
     o.cols = min(kGradN, p.k - o.c0);
     o.width = kGradN;
     o.kb0 = first[o.expert];
     o.nkb = first[o.expert + 1] - o.kb0;
     return true;
   }
-  if (t >= static_cast<int64_t>(first[p.experts]) * p.tiles_m) return false;
-  const int g = static_cast<int>(t / p.tiles_m);
+  if (t >= first[p.experts] * tiles_m) return false;
+  const int g = static_cast<int>(t / tiles_m);
   int lo = 0, hi = p.experts;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -135,15 +137,15 @@ __device__ __forceinline__ bool decode(const Fp8Args& p, const int32_t* first, c
   // Within an expert: groups of kTokenGroup token tiles sweep over w
   // together, so that w is read from HBM once per group.
   const int tiles = first[lo + 1] - first[lo];
-  const int64_t l = t - static_cast<int64_t>(first[lo]) * p.tiles_m;
-  const int group = static_cast<int>(l / (kTokenGroup * p.tiles_m));
-  const int r = static_cast<int>(l - static_cast<int64_t>(group) * kTokenGroup * p.tiles_m);
-  const int in_group = min(kTokenGroup, tiles - group * kTokenGroup);
-  const int tm = r / in_group;
-  const int i = group * kTokenGroup + (r - tm * in_group);
+  const uint32_t l = t - first[lo] * tiles_m;
+  const uint32_t group = l / (kTokenGroup * tiles_m);
+  const uint32_t r = l - group * kTokenGroup * tiles_m;
+  const uint32_t in_group = min(kTokenGroup, tiles - static_cast<int>(group) * kTokenGroup);
+  const uint32_t tm = r / in_group;
+  const int i = static_cast<int>(group * kTokenGroup + (r - tm * in_group));
   const int m = start[lo + 1] - start[lo];
   o.expert = lo;
-  o.n0 = tm * kTileM;
+  o.n0 = static_cast<int>(tm) * kTileM;
   o.width = ((m + tiles - 1) / tiles + kWidthUnit - 1) / kWidthUnit * kWidthUnit;
   o.c0 = start[lo] + i * o.width;
   o.cols = min(o.width, m - i * o.width);
@@ -209,14 +211,14 @@ __device__ __forceinline__ void scan_experts(const Fp8Args& p, int32_t* first, i
 
 // Walks the sets of scales of a pair's tiles.
 struct SetCursor {
-  int64_t t;
+  uint32_t t;
   Tile o;
   int kb;               // first K block of the set
   bool live;
 
   template <bool GRAD>
   __device__ __forceinline__ void begin(const Fp8Args& p, const int32_t* first, const int32_t* start,
-                                        int64_t t0) {
+                                        uint32_t t0) {
     t = t0;
     kb = 0;
     live = decode<GRAD>(p, first, start, t, o);
@@ -301,6 +303,7 @@ template <bool GRAD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp8_product_kernel(const __grid_constant__ Maps maps, const Fp8Args p) {
   using L = Layout<GRAD>;
+  constexpr int kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -335,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(&tmem_full[a], 1);
-      ptx::mbar_init(&tmem_empty[a], 2 * kEpiWarps * 32);
+      ptx::mbar_init(&tmem_empty[a], 2 * kEpiWarps);
     }
     ptx::mbar_init(drain, 1);
     *abort_flag = 0;
@@ -367,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int issued = 0;
       bool ok = true;
       Tile o;
-      for (int64_t t = pair; ok && decode<GRAD>(p, first, start, t, o); t += npairs) {
+      for (uint32_t t = pair; ok && decode<GRAD>(p, first, start, t, o); t += npairs) {
         const int half = o.width / 2;
         const int box = GRAD ? 0 : o.width / kWidthUnit - 1;
         const uint32_t b_bytes = static_cast<uint32_t>(half * kBK);
@@ -422,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t a_desc0 = ptx::smem_desc_sw128(ptx::smem_addr(smem), 16, 1024);
       const uint64_t s_desc0 = ptx::smem_desc_scales(ptx::smem_addr(smem + L::kScaleAt));
       Tile o;
-      for (int64_t t = pair; ok && decode<GRAD>(p, first, start, t, o); t += npairs) {
+      for (uint32_t t = pair; ok && decode<GRAD>(p, first, start, t, o); t += npairs) {
         if (o.nkb == 0) continue;
         if (!ptx::mbar_wait_cluster(&tmem_empty[acc], acc_phase ^ 1u, abort_flag)) {
           ok = false;
@@ -500,10 +503,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t acc_phase = 0;
     const uint32_t empty_leader0 = ptx::mapa_shared(ptx::smem_addr(&tmem_empty[0]), 0);
     const uint32_t empty_leader1 = ptx::mapa_shared(ptx::smem_addr(&tmem_empty[1]), 0);
-    uint8_t* stage_out = smem + L::kOutAt + (warp - 2) * 2 * L::kOutBuf;
+    uint8_t* stage_out = smem + L::kOutAt + (warp - 2) * L::kOutBufs * L::kOutBuf;
     int issued = 0;
     Tile o;
-    for (int64_t t = pair; decode<GRAD>(p, first, start, t, o); t += npairs) {
+    for (uint32_t t = pair; decode<GRAD>(p, first, start, t, o); t += npairs) {
       const int row0 = o.n0 + static_cast<int>(rank) * kHalfM + quad * 32;
       const bool empty_sum = o.nkb == 0;
       if (empty_sum && p.accumulate) continue;
@@ -531,13 +534,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 32; ++j) v[j] = 0u;
         }
         if (GRAD && row0 >= p.n) continue;
-        uint8_t* buf = stage_out + (issued & 1) * L::kOutBuf;
+        uint8_t* buf = stage_out + (issued % L::kOutBufs) * L::kOutBuf;
         ++issued;
         if (GRAD) {
           // 32 rows x 128 bytes, 16-byte chunk q of row r at q ^ (r & 7): the
           // output map's 128-byte swizzle.  A buffer is free once the store
-          // before the last has read it.
-          if (lane == 0) ptx::bulk_wait_read<1>();
+          // issued from it has read it.
+          if (lane == 0) ptx::bulk_wait_read<L::kOutBufs - 1>();
           __syncwarp();
 #pragma unroll
           for (int q = 0; q < 8; ++q)
@@ -571,8 +574,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (!empty_sum) {
+        // Every value has been read into registers and staged.
         ptx::tc_fence_before();
-        ptx::mbar_arrive_cluster(acc ? empty_leader1 : empty_leader0);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(acc ? empty_leader1 : empty_leader0);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
@@ -677,6 +682,7 @@ cudaError_t launch(const Maps& maps, const Fp8Args& p, int64_t max_tiles, int nu
   if (pairs > num_sms / 2) pairs = num_sms / 2;
   if (pairs > max_tiles) pairs = max_tiles;
   if (pairs < 1) pairs = 1;
+  if (max_tiles + 2 * pairs >= INT32_MAX) return cudaErrorInvalidValue;   // tile numbers are 32 bits
   return launch_pdl(fp8_product_kernel<GRAD>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads),
                     Layout<GRAD>::kSmem, s, maps, p);
 }
