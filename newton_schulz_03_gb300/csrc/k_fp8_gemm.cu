@@ -118,9 +118,11 @@ __device__ __forceinline__ bool decode(const Fp8Args& p, const int32_t* first, c
     o.expert = static_cast<int>(t / per);
     if (o.expert >= p.experts) return false;
     const uint32_t l = t - o.expert * per;
-    const uint32_t tn = l / tiles_m;
-    o.n0 = static_cast<int>(l - tn * tiles_m) * kTileM;
-    o.c0 = static_cast<int>(tn) * kGradN;
+    // Along a row of tiles first: the pairs running at one time then write
+    // whole rows of dw.
+    const uint32_t tm = l / p.tiles_n;
+    o.n0 = static_cast<int>(tm) * kTileM;
+    o.c0 = static_cast<int>(l - tm * p.tiles_n) * kGradN;
     o.cols = min(kGradN, p.k - o.c0);
     o.width = kGradN;
     o.kb0 = first[o.expert];
