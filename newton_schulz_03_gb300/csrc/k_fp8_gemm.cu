@@ -53,7 +53,7 @@ constexpr int kSets = 4;                          // sets in the ring
 constexpr int kScaleBytes = 512 + 1024;           // per set: 128 A cells, 256 B cells
 constexpr int kMaxTokens = 224;                   // rows: widest token tile
 constexpr int kWidthUnit = 32;                    // MMA columns come in multiples of this
-constexpr int kGradN = 192;                       // wgrad: columns per tile (a multiple of 32)
+constexpr int kGradN = 224;                       // wgrad: columns per tile (a multiple of 32)
 constexpr int kTokenGroup = 8;                    // rows: token tiles that share a sweep over w
 constexpr int kTmemCols = 512;
 constexpr int kTmemScales = 448;
