@@ -588,25 +588,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ scales (both CTAs)
-    // Warp `which` fills the sets which, which + 2, ...; the loads of its next
-    // set are in flight while the current one waits for its place.
+    // Warp `which` fills the sets which, which + 2, ...; a set's loads are in
+    // flight while it waits for its place.  They follow the arrival for the set
+    // before: a release waits for its thread's loads too.
     const int which = warp - 2 - kEpiWarps;
     SetCursor at{};
     at.begin<GRAD>(p, first, start, pair);
     at.settle<GRAD>(p, first, start, npairs);
     if (which == 1 && at.live) at.next<GRAD>(p, first, start, npairs);
-    uint32_t cells[12];
-    if (at.live) load_set<GRAD>(p, at, rank, lane, cells);
     int set = which;
     uint32_t set_phase = 0;
     bool ok = true;
     while (at.live) {
-      uint32_t now[12];
-#pragma unroll
-      for (int i = 0; i < 12; ++i) now[i] = cells[i];
+      uint32_t cells[12];
+      load_set<GRAD>(p, at, rank, lane, cells);
       at.next<GRAD>(p, first, start, npairs);
       if (at.live) at.next<GRAD>(p, first, start, npairs);
-      if (at.live) load_set<GRAD>(p, at, rank, lane, cells);
       const bool got = ptx::mbar_wait_cluster(&set_empty[set], set_phase ^ 1u, abort_flag);
       if (!__all_sync(0xffffffffu, got)) {
         ok = false;
@@ -614,9 +611,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // Lane l's 16 bytes hold the cells of rows l, l + 32, l + 64, l + 96.
       uint4* to = reinterpret_cast<uint4*>(smem + L::kScaleAt + set * kScaleBytes);
-      to[lane] = make_uint4(now[0], now[1], now[2], now[3]);
-      to[32 + lane] = make_uint4(now[4], now[5], now[6], now[7]);
-      to[64 + lane] = make_uint4(now[8], now[9], now[10], now[11]);
+      to[lane] = make_uint4(cells[0], cells[1], cells[2], cells[3]);
+      to[32 + lane] = make_uint4(cells[4], cells[5], cells[6], cells[7]);
+      to[64 + lane] = make_uint4(cells[8], cells[9], cells[10], cells[11]);
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&set_full[set]), 0));
