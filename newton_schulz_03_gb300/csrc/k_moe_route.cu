@@ -65,14 +65,11 @@ struct Elem<__nv_bfloat16> {
   }
 };
 
-// A number that orders as the float does; 0 (below every finite one) stands
-// for a closed expert.  -0 is made +0 first, so that the two tie.
-__device__ __forceinline__ uint32_t ordered(float v) {
-  const uint32_t u = __float_as_uint(v + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float unordered(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+// Largest of the warp's values (a NaN does not take part).
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -83,6 +80,17 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // 1 / (1 + exp(-x)), each operation rounded to FP32.
 __device__ __forceinline__ float sigmoid(float x) { return __frcp_rn(1.0f + expf(-x)); }
+
+// The same within 4e-7, in four instructions: for telling which experts cannot
+// be among the chosen.  (The exponential's argument is rounded once, |x| 6e-8 of
+// it, which the sigmoid's slope s (1 - s) takes below 2e-8; the two approximate
+// instructions and the sum are within 2^-22 each.)
+__device__ __forceinline__ float sigmoid_near(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.442695041f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
 
 __device__ __forceinline__ bool is_open(float x) { return fabsf(x) <= FLT_MAX; }
 
@@ -109,163 +117,353 @@ __device__ __forceinline__ void load_row(const T* row, int experts, int lane, fl
   }
 }
 
-// The warp's best (key, expert) given each lane's best; ties: lowest expert.
-__device__ __forceinline__ void warp_best(uint32_t& key, int& e) {
-  const uint32_t top = __reduce_max_sync(kAll, key);
-  e = __reduce_min_sync(kAll, key == top ? e : INT32_MAX);
-  key = top;
+// Lane of the warp's largest value, the first of equal ones; -1 when all are
+// -inf.  `top` receives the value.
+__device__ __forceinline__ int warp_best_lane(float v, float& top) {
+  top = warp_max(v);
+  if (!(top > -INFINITY)) return -1;
+  return __ffs(__ballot_sync(kAll, v == top)) - 1;
 }
 
-// Values of the groups, group g's in lane g: the ordered sum of its best
-// group_top open experts' choice values, 0 where none is open.
-__device__ __forceinline__ uint32_t group_key(uint32_t first, uint32_t second, int group_top) {
-  if (first == 0u) return 0u;
-  const float f = unordered(first);
-  return ordered(group_top == 2 && second != 0u ? f + unordered(second) : f);
+// Value of a group from its best two choice values (-inf: closed).
+__device__ __forceinline__ float group_value(float first, float second, int group_top) {
+  return group_top == 2 && second > -INFINITY ? first + second : first;
 }
 
-// Groups of `lanes` = 1, 2, 4 .. 32 neighbouring lanes of a vector: the best
-// two by a butterfly, then every group's key to its lane.
+// Groups of `lanes` = 1, 2, 4 .. 32 neighbouring lanes of a vector of 128
+// experts: the best two by a butterfly, then every group's value to its lane.
 template <int R>
-__device__ __forceinline__ uint32_t group_keys_by_lanes(const uint32_t (&key)[R], int lanes,
-                                                        int groups, int group_top, int lane) {
-  const int per_vector = 32 / lanes;              // groups in one vector of 128 experts
-  uint32_t mine = 0u;
+__device__ __forceinline__ float group_values_by_lanes(const float (&c)[R], int lanes, int groups,
+                                                       int group_top, int lane) {
+  const int per_vector = 32 / lanes;              // groups in one vector
+  float mine = -INFINITY;
 #pragma unroll
   for (int i = 0; i < R / 4; ++i) {
     if (i * per_vector >= groups) break;
-    const uint32_t a = key[4 * i], b = key[4 * i + 1], c = key[4 * i + 2], d = key[4 * i + 3];
-    const uint32_t hi0 = max(a, b), lo0 = min(a, b), hi1 = max(c, d), lo1 = min(c, d);
-    uint32_t first = max(hi0, hi1);
-    uint32_t second = max(min(hi0, hi1), hi0 > hi1 ? lo0 : lo1);
+    const float hi0 = fmaxf(c[4 * i], c[4 * i + 1]), lo0 = fminf(c[4 * i], c[4 * i + 1]);
+    const float hi1 = fmaxf(c[4 * i + 2], c[4 * i + 3]), lo1 = fminf(c[4 * i + 2], c[4 * i + 3]);
+    float first = fmaxf(hi0, hi1);
+    float second = fmaxf(fminf(hi0, hi1), hi0 > hi1 ? lo0 : lo1);
     for (int o = 1; o < lanes; o <<= 1) {
-      const uint32_t f = __shfl_xor_sync(kAll, first, o), q = __shfl_xor_sync(kAll, second, o);
-      second = max(min(first, f), max(second, q));
-      first = max(first, f);
+      const float f = __shfl_xor_sync(kAll, first, o), q = __shfl_xor_sync(kAll, second, o);
+      second = fmaxf(fminf(first, f), fmaxf(second, q));
+      first = fmaxf(first, f);
     }
-    const uint32_t g = __shfl_sync(kAll, group_key(first, second, group_top),
-                                   (lane % per_vector) * lanes);
+    const float g = __shfl_sync(kAll, group_value(first, second, group_top), (lane % per_vector) * lanes);
     if (lane / per_vector == i) mine = g;
   }
-  return lane < groups ? mine : 0u;
+  return lane < groups ? mine : -INFINITY;
 }
 
 // Any group size: lane g walks group g in shared memory, each lane starting
 // elsewhere (distinct banks).
-__device__ __forceinline__ uint32_t group_keys_by_walk(const uint32_t* keys, int size, int groups,
-                                                       int group_top, int lane) {
-  if (lane >= groups) return 0u;
-  uint32_t first = 0u, second = 0u;
+__device__ __forceinline__ float group_values_by_walk(const float* values, int size, int groups,
+                                                      int group_top, int lane) {
+  if (lane >= groups) return -INFINITY;
+  float first = -INFINITY, second = -INFINITY;
   int j = lane % size;
   for (int i = 0; i < size; ++i) {
-    const uint32_t v = keys[lane * size + j];
-    second = max(second, min(first, v));
-    first = max(first, v);
+    const float v = values[lane * size + j];
+    second = fmaxf(second, fminf(first, v));
+    first = fmaxf(first, v);
     if (++j == size) j = 0;
   }
-  return group_key(first, second, group_top);
+  return group_value(first, second, group_top);
 }
 
-// The k largest of the lanes' keys over the warp, ties to the lowest expert;
-// returns the j-th one's expert in lane j (-1: fewer than k are open).  A
-// lane's keys lie in order of expert.  The k-th largest of the lanes' maxima is
-// a lower bound of the k-th largest key: only the few keys that reach it are
-// gathered, one per lane, and ranked by counting.
-template <int R>
-__device__ __forceinline__ int choose(uint32_t (&key)[R], const int (&expert)[R], int k, int lane,
-                                      uint2* list) {
-  uint32_t most = 0u;
+// A token's routing state that does not depend on the expert.
+struct Row {
+  const void* logits;
+  const float* bias;
+  float top, denom;      // softmax
+  bool by_logit;
+};
+
+// Choice value of one expert from its logit, in FP32 as written.
+template <bool SOFTMAX>
+__device__ __forceinline__ float choice_value(const Row& w, float x, int e) {
+  if (w.by_logit) return x;
+  const float s = SOFTMAX ? expf(x - w.top) / w.denom : sigmoid(x);
+  return w.bias != nullptr ? s + w.bias[e] : s;
+}
+
+struct Choice {
+  int id;                // -1: none
+  float x;               // its logit
+};
+
+// A candidate's choice value and expert as one ordered number: the larger
+// value, of equal ones the lower expert.  0 is below every one.
+using Candidate = unsigned long long;
+__device__ __forceinline__ Candidate candidate(float c, int e) {
+  const uint32_t u = __float_as_uint(c + 0.0f);   // -0 ties with +0
+  const uint32_t ordered = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return (static_cast<unsigned long long>(ordered) << 32) | static_cast<uint32_t>(~e);
+}
+
+// The k best of the lanes' values, ties to the lowest expert: the j-th one in
+// lane j.  near: the values are within the tolerance of the choice values only.
+// The k-th largest of the lanes' maxima bounds the k-th largest value from
+// below, so only the few values that reach it (less the tolerance, twice) can be
+// chosen; they are gathered one per lane, valued exactly and ranked by counting.
+// false: more than 32 reach it.
+template <typename T, int R, bool SOFTMAX, typename ExpertOf>
+__device__ __forceinline__ bool choose(const Row& w, const float (&c)[R], ExpertOf expert, bool near,
+                                       int k, int lane, Candidate* list, Choice& out) {
+  float most = c[0];
 #pragma unroll
-  for (int r = 0; r < R; ++r) most = max(most, key[r]);
-  uint32_t bound = 1u, left = most;               // no closed expert reaches 1
+  for (int r = 1; r < R; ++r) most = fmaxf(most, c[r]);
+  float bound = -FLT_MAX, left = most;
   for (int got = 0; got < k;) {
-    const uint32_t top = __reduce_max_sync(kAll, left);
-    if (top == 0u) {
-      bound = 1u;
+    const float top = warp_max(left);
+    if (!(top > -INFINITY)) {
+      bound = -FLT_MAX;
       break;
     }
     bound = top;
     const bool is_top = left == top;
     got += __popc(__ballot_sync(kAll, is_top));
-    if (is_top) left = 0u;
+    if (is_top) left = -INFINITY;
   }
-  // Places of this lane's candidates.
-  int mine = 0;
+  if (near && bound > -FLT_MAX) {
+    bound -= 2e-6f + 1e-6f * fabsf(bound);
+    if (!(bound > -FLT_MAX)) return false;        // biases beyond any sense
+  }
+  uint32_t reach = 0u;
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-    mine += key[r] >= bound ? 1 : 0;
-  int end = mine;
+  for (int r = 0; r < R; ++r) reach |= c[r] >= bound ? 1u << r : 0u;
+  int end = __popc(reach);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(kAll, end, o);
     if (lane >= o) end += v;
   }
   const int total = __shfl_sync(kAll, end, 31);
-  if (total <= 32) {
-    int at = end - mine;
-    if (mine > 0) {
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (key[r] >= bound) list[at++] = make_uint2(key[r], static_cast<uint32_t>(expert[r]));
-    }
-    __syncwarp();
-    uint2 own = make_uint2(0u, 0u);
-    if (lane < total) own = list[lane];
-    int rank = 0;
-    for (int j = 0; j < total; ++j) {
-      const uint2 other = list[j];
-      rank += other.x > own.x || (other.x == own.x && other.y < own.y) ? 1 : 0;
-    }
-    __syncwarp();
-    if (lane < total) list[rank].y = own.y;       // ranks are distinct
-    __syncwarp();
-    return lane < min(k, total) ? static_cast<int>(list[lane].y) : -1;
+  if (total > 32) return false;
+  int* experts = reinterpret_cast<int*>(list);
+  for (int at = end - __popc(reach); reach != 0u; reach &= reach - 1u, ++at)
+    experts[at] = expert(__ffs(reach) - 1);
+  __syncwarp();
+  int e = 0;
+  float x = 0.f;
+  Candidate own = 0ull;
+  if (lane < total) {
+    e = experts[lane];
+    x = Elem<T>::load(static_cast<const T*>(w.logits) + e);
+    own = candidate(choice_value<SOFTMAX>(w, x, e), e);
   }
-  // Many equal keys: k rounds of the warp's best one.
-  int id = -1;
+  __syncwarp();
+  list[lane] = own;
+  __syncwarp();
+  int rank = 0;
+  for (int j = 0; j < total; j += 4) {            // past the end: zeros
+    const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(list + j);
+    const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(list + j + 2);
+    rank += (p.x > own ? 1 : 0) + (p.y > own ? 1 : 0) + (q.x > own ? 1 : 0) + (q.y > own ? 1 : 0);
+  }
+  __syncwarp();
+  float2* place = reinterpret_cast<float2*>(list);
+  if (lane < total) place[rank] = make_float2(x, __int_as_float(e));   // ranks are distinct
+  __syncwarp();
+  out.id = -1;
+  if (lane < min(k, total)) {
+    const float2 v = place[lane];
+    out.x = v.x;
+    out.id = __float_as_int(v.y);
+  }
+  return true;
+}
+
+// The same by k rounds of the warp's best, for rows with many equal values;
+// c holds the exact choice values.
+template <typename T, int R, typename ExpertOf>
+__device__ __forceinline__ void choose_by_rounds(const Row& w, float (&c)[R], ExpertOf expert, int k,
+                                                 int lane, Choice& out) {
+  out.id = -1;
   for (int j = 0; j < k; ++j) {
-    uint32_t best = 0u;
+    float best = -INFINITY;
     int e = INT32_MAX;
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (key[r] > best) {
-        best = key[r];
-        e = expert[r];
+      if (c[r] > best) {                          // a lane's experts are in order
+        best = c[r];
+        e = expert(r);
       }
-    warp_best(best, e);
-    if (best == 0u) break;
-    if (lane == j) id = e;
+    const float top = warp_max(best);
+    if (!(top > -INFINITY)) break;
+    e = __reduce_min_sync(kAll, best == top ? e : INT32_MAX);
+    if (lane == j) out.id = e;
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (expert[r] == e) key[r] = 0u;
+      if (expert(r) == e) c[r] = -INFINITY;
   }
-  return id;
+  if (out.id >= 0) out.x = Elem<T>::load(static_cast<const T*>(w.logits) + out.id);
 }
 
-// choose() among the n experts of the listed groups (n <= 32 R).
-template <int R>
-__device__ __forceinline__ int choose_of(const uint32_t* keys, const int* groups, int size, int n,
-                                         int k, int lane, uint2* list) {
-  uint32_t key[R];
-  int expert[R];
+// Either way; false: not certain from near values.
+template <typename T, int R, bool SOFTMAX, typename ExpertOf>
+__device__ __forceinline__ bool choose_any(const Row& w, float (&c)[R], ExpertOf expert, bool near,
+                                           int k, int lane, Candidate* list, Choice& out) {
+  if (choose<T, R, SOFTMAX>(w, c, expert, near, k, lane, list, out)) return true;
+  if (near) return false;
+  choose_by_rounds<T, R>(w, c, expert, k, lane, out);
+  return true;
+}
+
+// Among the n experts of the listed groups (n <= 32 R), in order over the lanes.
+template <typename T, int R, bool SOFTMAX>
+__device__ __forceinline__ bool choose_of(const Row& w, const float* values, const int* groups,
+                                          int size, uint32_t per_group, int n, bool near, int k,
+                                          int lane, Candidate* list, Choice& out) {
+  float c[R];
+  const auto expert = [&](int r) {
+    const int i = r * 32 + lane;
+    const int g = per_group == 0u ? i : static_cast<int>(__umulhi(i, per_group));
+    return i < n ? groups[g] * size + (i - g * size) : INT32_MAX;
+  };
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int c = r * 32 + lane;
-    key[r] = 0u;
-    expert[r] = INT32_MAX;
-    if (c < n) {
-      const int g = c / size;
-      expert[r] = groups[g] * size + (c - g * size);
-      key[r] = keys[expert[r]];
-    }
+    c[r] = -INFINITY;
+    if (r * 32 + lane < n) c[r] = values[expert(r)];
   }
-  return choose<R>(key, expert, k, lane, list);
+  return choose_any<T, R, SOFTMAX>(w, c, expert, near, k, lane, list, out);
 }
 
-template <typename T, int V, int R>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
-  extern __shared__ uint32_t smem_keys[];
-  __shared__ uint2 lists[kWarps][32];
+// Shared memory of one warp's token.
+struct Scratch {
+  Candidate* list;       // [32]
+  int* groups;           // [kMoeMaxGroups]
+  float* values;         // [experts], with groups
+};
+
+// One token's choice.  NEAR: from near sigmoids (false: they do not settle it).
+template <typename T, int V, int R, bool SOFTMAX, bool GROUPS, bool NEAR>
+__device__ __forceinline__ bool route_row(const RouteArgs& a, Row& w, int lane, const Scratch& sc,
+                                          Choice& mine) {
+  float c[R];
+  load_row<T, V, R>(static_cast<const T*>(w.logits), a.experts, lane, c);
+  // Whether every logit (and bias) is finite: v * 0 is NaN otherwise.
+  const bool whole = a.experts == 32 * R;
+  float z = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (whole || expert_of<V>(r, lane) < a.experts) z = fmaf(c[r], 0.f, z);
+  uint32_t closed = 0u;                           // registers of closed experts
+  if (!__all_sync(kAll, z == 0.f) || !whole) {
+    bool bad = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (!is_open(c[r])) {
+        bad = bad || !(c[r] < 0.f);               // NaN or +inf: closed, and reported
+        c[r] = -INFINITY;
+        closed |= 1u << r;
+      }
+    if (bad) atomicOr(a.err, kDevErrInput);
+  }
+  if (SOFTMAX) {
+    // Statistics over the open experts: a closed one's exp is 0.
+    w.top = -FLT_MAX;
+    w.denom = 0.f;
+    if (!(w.by_logit && a.renorm)) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) w.top = fmaxf(w.top, c[r]);
+      w.top = warp_max(w.top);
+#pragma unroll
+      for (int r = 0; r < R; ++r) w.denom += expf(c[r] - w.top);
+      w.denom = warp_sum(w.denom);
+    }
+    if (!w.by_logit) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) c[r] = expf(c[r] - w.top) / w.denom;
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) c[r] = NEAR ? sigmoid_near(c[r]) : sigmoid(c[r]);
+  }
+  if (a.bias != nullptr) {
+    float b[R];
+    load_row<float, V, R>(a.bias, a.experts, lane, b);
+    z = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (whole || expert_of<V>(r, lane) < a.experts) z = fmaf(b[r], 0.f, z);
+      c[r] += b[r];
+    }
+    if (!__all_sync(kAll, z == 0.f)) {            // a NaN bias closes
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (c[r] != c[r]) closed |= 1u << r;
+    }
+  }
+  if (__any_sync(kAll, closed != 0u)) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if ((closed >> r) & 1u) c[r] = -INFINITY;
+  }
+
+  if constexpr (!GROUPS) {
+    const auto expert = [&](int r) { return expert_of<V>(r, lane); };
+    return choose_any<T, R, SOFTMAX>(w, c, expert, NEAR, a.k, lane, sc.list, mine);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; r += V) {
+      const int e = expert_of<V>(r, lane);
+      if (e >= a.experts) continue;
+      if (V == 4)
+        *reinterpret_cast<float4*>(sc.values + e) =
+            make_float4(c[r], c[(r + 1) % R], c[(r + 2) % R], c[(r + 3) % R]);
+      else
+        sc.values[e] = c[r];
+    }
+    __syncwarp();
+    const int size = a.group_size;
+    const int lanes = size / 4;                     // of a group within a vector
+    float gv;
+    if (V == 4 && size % 4 == 0 && lanes <= 32 && (lanes & (lanes - 1)) == 0)
+      gv = group_values_by_lanes<R>(c, lanes, a.groups, a.group_top, lane);
+    else
+      gv = group_values_by_walk(sc.values, size, a.groups, a.group_top, lane);
+    uint32_t stay = 0u;
+    float last = INFINITY;
+    for (int i = 0; i < a.top_groups; ++i) {
+      float v;
+      const int g = warp_best_lane(gv, v);
+      if (g < 0) break;
+      last = v;
+      stay |= 1u << g;
+      if (lane == g) gv = -INFINITY;
+    }
+    // Near values settle the groups when the next one is well below: two values
+    // of each are off by the tolerance.
+    if (NEAR) {
+      const float next = warp_max(gv);
+      if (next > -INFINITY && !(last - next > 8e-6f + 4e-6f * fabsf(last))) return false;
+    }
+    if ((stay >> lane) & 1u) sc.groups[__popc(stay & ((1u << lane) - 1u))] = lane;
+    __syncwarp();
+    const int n = __popc(stay) * size;
+    if (n <= 8 * R)
+      return choose_of<T, R / 4, SOFTMAX>(w, sc.values, sc.groups, size, a.per_group, n, NEAR, a.k,
+                                          lane, sc.list, mine);
+    return choose_of<T, R, SOFTMAX>(w, sc.values, sc.groups, size, a.per_group, n, NEAR, a.k, lane,
+                                    sc.list, mine);
+  }
+}
+
+// The exact second look at a token, rarely taken: out of line.
+template <typename T, int V, int R, bool GROUPS>
+__device__ __noinline__ Choice route_row_again(const RouteArgs& a, Row w, int lane, Scratch sc) {
+  Choice mine;
+  __syncwarp();
+  route_row<T, V, R, false, GROUPS, false>(a, w, lane, sc, mine);
+  return mine;
+}
+
+template <typename T, int V, int R, bool SOFTMAX, bool GROUPS>
+__global__ void __launch_bounds__(kWarps * 32, R <= 16 ? 8 : 4)
+    route_kernel(const __grid_constant__ RouteArgs a) {
+  extern __shared__ float smem_values[];
+  __shared__ __align__(16) Candidate lists[kWarps][32];
   __shared__ int group_list[kWarps][kMoeMaxGroups];
   grid_dep_wait();
   grid_dep_launch();
@@ -281,132 +479,38 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
     }
     return;
   }
-  float x[R];
-  load_row<T, V, R>(static_cast<const T*>(a.logits) + t * a.experts, a.experts, lane, x);
+  Row w;
+  w.logits = static_cast<const T*>(a.logits) + t * a.experts;
+  w.bias = a.bias;
+  w.by_logit = SOFTMAX && a.bias == nullptr && a.group_top == 1;
+  const Scratch sc{lists[warp], group_list[warp], smem_values + (GROUPS ? warp * a.experts : 0)};
+  // Sigmoids are first taken near: hundreds of them written out in FP32 cost
+  // more than all the rest, and only the chosen ones' last bits matter.
+  Choice mine;
+  if (!route_row<T, V, R, SOFTMAX, GROUPS, !SOFTMAX>(a, w, lane, sc, mine))
+    mine = route_row_again<T, V, R, GROUPS>(a, w, lane, sc);
+  const int my_id = mine.id;
+  const float top = w.top, denom = w.denom;
 
-  // Whether every logit is finite: x * 0 is NaN otherwise.
-  const bool whole = a.experts == 32 * R;
-  float z = 0.f;
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (whole || expert_of<V>(r, lane) < a.experts) z = fmaf(x[r], 0.f, z);
-  const bool finite = __all_sync(kAll, z == 0.f);
-  if (!finite) {
-    bool bad = false;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (!is_open(x[r])) {
-        bad = bad || !(x[r] < 0.f);   // NaN or +inf: closed, and reported
-        x[r] = -INFINITY;
-      }
-    if (bad) atomicOr(a.err, kDevErrInput);
-  }
-  // Softmax statistics; a closed expert's exp is 0.
-  float top = -FLT_MAX, denom = 0.f;
-  const bool by_logit = a.softmax && a.bias == nullptr && a.group_top == 1;
-  if (a.softmax && !(by_logit && a.renorm)) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) top = fmaxf(top, x[r]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-#pragma unroll
-    for (int r = 0; r < R; ++r) denom += expf(x[r] - top);
-    denom = warp_sum(denom);
-  }
-
-  // Choice values as ordered numbers.
-  uint32_t key[R];
-  int expert[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) expert[r] = expert_of<V>(r, lane);
-  float c[R];
-  if (by_logit) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) c[r] = x[r];
-  } else if (a.softmax) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) c[r] = expf(x[r] - top) / denom;
-  } else {
-#pragma unroll
-    for (int r = 0; r < R; ++r) c[r] = sigmoid(x[r]);
-  }
-  if (a.bias != nullptr) {
-    float b[R];
-    load_row<float, V, R>(a.bias, a.experts, lane, b);
-#pragma unroll
-    for (int r = 0; r < R; ++r) c[r] += b[r];
-  }
-#pragma unroll
-  for (int r = 0; r < R; ++r) key[r] = ordered(c[r]);
-  if (!(finite && whole)) {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (!(x[r] > -INFINITY) || c[r] != c[r]) key[r] = 0u;
-  }
-  int my_id = -1;
-
-  if (a.groups > 1) {
-    uint32_t* keys = smem_keys + warp * a.experts;
-#pragma unroll
-    for (int r = 0; r < R; r += V) {
-      const int e = expert_of<V>(r, lane);
-      if (e >= a.experts) continue;
-      if (V == 4)
-        *reinterpret_cast<uint4*>(keys + e) =
-            make_uint4(key[r], key[(r + 1) % R], key[(r + 2) % R], key[(r + 3) % R]);
-      else
-        keys[e] = key[r];
-    }
-    __syncwarp();
-    const int size = a.experts / a.groups;
-    const int lanes = size / 4;                   // of a group within a vector
-    uint32_t gkey;
-    if (V == 4 && size % 4 == 0 && lanes <= 32 && (lanes & (lanes - 1)) == 0)
-      gkey = group_keys_by_lanes<R>(key, lanes, a.groups, a.group_top, lane);
-    else
-      gkey = group_keys_by_walk(keys, size, a.groups, a.group_top, lane);
-    uint32_t stay = 0u;
-    for (int i = 0; i < a.top_groups; ++i) {
-      uint32_t best = gkey;
-      int g = lane;
-      warp_best(best, g);
-      if (best == 0u) break;
-      stay |= 1u << g;
-      if (lane == g) gkey = 0u;
-    }
-    // The groups' experts, in order, spread over the lanes anew.
-    if ((stay >> lane) & 1u) group_list[warp][__popc(stay & ((1u << lane) - 1u))] = lane;
-    __syncwarp();
-    const int n = __popc(stay) * size;
-    if (n <= 8 * R) {
-      my_id = choose_of<R / 4>(keys, group_list[warp], size, n, a.k, lane, lists[warp]);
-    } else {
-      my_id = choose_of<R>(keys, group_list[warp], size, n, a.k, lane, lists[warp]);
-    }
-  } else {
-    my_id = choose<R>(key, expert, a.k, lane, lists[warp]);
-  }
-
-  // Lane j holds the j-th choice; its logit is in L1.
+  // Lane j holds the j-th choice.
   float s = 0.f;
-  const float xj = my_id >= 0 ? Elem<T>::load(static_cast<const T*>(a.logits) + t * a.experts + my_id)
-                              : -INFINITY;
-  if (a.softmax && a.renorm) {
+  const float xj = my_id >= 0 ? mine.x : -INFINITY;
+  if (SOFTMAX && a.renorm) {
     float m = xj;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
     s = my_id >= 0 ? expf(xj - m) : 0.f;
   } else if (my_id >= 0) {
-    s = a.softmax ? expf(xj - top) / denom : sigmoid(xj);
+    s = SOFTMAX ? expf(xj - top) / denom : sigmoid(xj);
   }
-  float w = s;
+  float share = s;
   if (a.renorm) {
     const float sum = warp_sum(s);
-    w = sum > 0.f ? s / sum : 0.f;     // every chosen score underflowed: no weight
+    share = sum > 0.f ? s / sum : 0.f;   // every chosen score underflowed: no weight
   }
   if (lane < a.k) {
     ids[lane] = my_id;
-    weights[lane] = w * a.scale;
+    weights[lane] = share * a.scale;
   }
 }
 
@@ -516,23 +620,26 @@ cudaError_t launch_rv(const RouteArgs& a, bool backward, cudaStream_t s) {
   const int64_t blocks = (a.tokens + kWarps - 1) / kWarps;
   const dim3 grid(static_cast<unsigned>(blocks)), block(kWarps * 32);
   if (backward) return launch_pdl(route_backward_kernel<T, V, R>, grid, block, 0, s, a);
-  const size_t smem = a.groups > 1 ? size_t(kWarps) * a.experts * 4 : 0;
-  return launch_pdl(route_kernel<T, V, R>, grid, block, smem, s, a);
+  if (a.groups > 1) {
+    const size_t smem = size_t(kWarps) * a.experts * 4;
+    return launch_pdl(a.softmax ? route_kernel<T, V, R, true, true> : route_kernel<T, V, R, false, true>,
+                      grid, block, smem, s, a);
+  }
+  return launch_pdl(a.softmax ? route_kernel<T, V, R, true, false> : route_kernel<T, V, R, false, false>,
+                    grid, block, 0, s, a);
 }
 
-// Registers per lane: the least power of two that holds the row.  Rows of a
+// Registers per lane: 4, 16 or 32, the least that holds the row.  Rows of a
 // multiple of four experts are read four at a time.
 template <typename T>
 cudaError_t launch_t(const RouteArgs& a, bool backward, cudaStream_t s) {
   const int per = (a.experts + 31) / 32;
   if (a.experts % 4 == 0) {
     if (per <= 4) return launch_rv<T, 4, 4>(a, backward, s);
-    if (per <= 8) return launch_rv<T, 4, 8>(a, backward, s);
     if (per <= 16) return launch_rv<T, 4, 16>(a, backward, s);
     return launch_rv<T, 4, 32>(a, backward, s);
   }
   if (per <= 4) return launch_rv<T, 1, 4>(a, backward, s);
-  if (per <= 16) return launch_rv<T, 1, 16>(a, backward, s);
   return launch_rv<T, 1, 32>(a, backward, s);
 }
 

@@ -25,6 +25,8 @@ struct RouteArgs {
   int32_t experts, k;
   int32_t softmax;         // 0: sigmoid scores
   int32_t groups, top_groups, group_top;
+  int32_t group_size;      // experts per group
+  uint32_t per_group;      // ceil(2^32 / experts per group): i * it >> 32 is i's group
   int32_t renorm;
   float scale;
   int* err;

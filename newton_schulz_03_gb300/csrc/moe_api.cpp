@@ -157,6 +157,9 @@ muon_status_t muon_moe_route(muon_handle_t h, int64_t tokens, int32_t experts, i
   // All groups chosen from: no groups.
   a.groups = opts->top_groups == opts->groups ? 1 : opts->groups;
   a.top_groups = opts->top_groups;
+  const uint32_t size = static_cast<uint32_t>(experts / a.groups);
+  a.group_size = static_cast<int32_t>(size);
+  a.per_group = size == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + size - 1) / size);
   a.group_top = a.groups == 1 ? 1 : opts->group_top;
   a.renorm = opts->renormalize != 0;
   a.scale = opts->scale;
