@@ -66,12 +66,13 @@ class ExpertLayer:
         self.q_down.update(self.h, self.down)
 
     # ---------------------------------------------------------------- pieces
-    def _rows(self, x, pos=None, rows=None):
-        """x in FP8 rows (sent to the rows pos[t] of the tokens' experts)."""
+    def _rows(self, x, pos=None, rows=None, offsets=None):
+        """x in FP8 rows (sent to the rows pos[t] of the tokens' experts; or
+        the experts' rows themselves)."""
         r, d = x.shape[0] if rows is None else rows, x.shape[1]
         q = torch.empty(r, d, dtype=F8, device=x.device)
         s = torch.empty(r, _blocks(d), dtype=torch.uint8, device=x.device)
-        ns.muon_fp8_quantize_rows(self.h, x, q, s, pos=pos)
+        ns.muon_fp8_quantize_rows(self.h, x, q, s, pos=pos, offsets=offsets)
         return q, s
 
     def _cols(self, x, offsets, rows, slots=None):
@@ -88,20 +89,21 @@ class ExpertLayer:
         return y
 
     # ---------------------------------------------------------------- passes
-    def forward(self, x):
-        """x [tokens, hidden] BF16 -> (y [tokens, hidden] BF16, what backward needs)."""
+    def forward(self, x, mask=None):
+        """x [tokens, hidden] BF16 -> (y [tokens, hidden] BF16, what backward needs).
+        Tokens whose mask is 0 (padding) go to no expert: y is 0 there."""
         t, k, dev = x.shape[0], self.top_k, x.device
         logits = x.float() @ self.router[0].t()
         ids = torch.empty(t, k, dtype=torch.int32, device=dev)
         w = torch.empty(t, k, device=dev)
-        ns.muon_moe_route(self.h, logits, ids, w, bias=self.bias)
+        ns.muon_moe_route(self.h, logits, ids, w, bias=self.bias, mask=mask)
         offsets = torch.empty(self.experts + 1, dtype=torch.int32, device=dev)
         slots = torch.empty(t * k, dtype=torch.int32, device=dev)
         pos = torch.empty(t, k, dtype=torch.int32, device=dev)
         ns.muon_moe_plan(self.h, ids, offsets, slots, pos)
         hidden = self._product(self._rows(x, pos, t * k), self.q_up.q, self.q_up.s, offsets)
         act = torch.relu(hidden).square()
-        y = self._product(self._rows(act), self.q_down.q, self.q_down.s, offsets)
+        y = self._product(self._rows(act, offsets=offsets), self.q_down.q, self.q_down.s, offsets)
         out = torch.empty_like(x)
         ns.muon_moe_combine(self.h, y, pos, w, out)
         return out, (x, logits, ids, w, offsets, slots, pos, hidden, act, y)
@@ -112,9 +114,9 @@ class ExpertLayer:
         rows = y.shape[0]
         g_y, g_w = torch.empty_like(y), torch.empty_like(w)
         ns.muon_moe_combine_backward(self.h, grad, y, pos, w, g_y, g_w)
-        g_act = self._product(self._rows(g_y), self.q_down.qt, self.q_down.st, offsets)
+        g_act = self._product(self._rows(g_y, offsets=offsets), self.q_down.qt, self.q_down.st, offsets)
         g_hidden = g_act * (2 * torch.relu(hidden))
-        g_rows = self._product(self._rows(g_hidden), self.q_up.qt, self.q_up.st, offsets)
+        g_rows = self._product(self._rows(g_hidden, offsets=offsets), self.q_up.qt, self.q_up.st, offsets)
         g_x = torch.empty_like(x)
         ns.muon_moe_combine(self.h, g_rows, pos, None, g_x)
         cols = self._cols(g_y, offsets, rows) + self._cols(act, offsets, rows)

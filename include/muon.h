@@ -514,10 +514,13 @@ muon_status_t muon_moe_combine_backward(muon_handle_t handle, int64_t tokens, in
  *
  * Rows: blocks run along a row of x [tokens][hidden] (BF16).  pos NULL: q
  * [tokens][hidden], scales [tokens][ceil(hidden / 128)].  Otherwise row t is
- * written to the rows pos[t][j] >= 0 of q and scales (`rows` of them). */
+ * written to the rows pos[t][j] >= 0 of q and scales (`rows` of them).
+ * live_rows: NULL, or one int32 on the device (offsets + experts, say): only
+ * that many first rows of x are read and written, whatever the others hold. */
 muon_status_t muon_fp8_quantize_rows(muon_handle_t handle, int64_t tokens, int32_t hidden,
                                      const uint16_t* x, const int32_t* pos, int32_t top_k,
-                                     int64_t rows, uint8_t* q, uint8_t* scales, void* stream);
+                                     int64_t rows, const int32_t* live_rows, uint8_t* q,
+                                     uint8_t* scales, void* stream);
 
 /* Weights w [experts][n][k] (w_type), one scale per 128 x 128 block: q
  * [experts][n][k] with scales [experts][ceil(n / 128)][ceil(k / 128)], and

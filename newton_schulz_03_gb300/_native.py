@@ -148,7 +148,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "muon_moe_combine_backward": (c_int, [c_vp, c_i64, c_i32, c_i64, c_i32, c_vp, c_vp, c_vp,
                                               c_vp, c_vp, c_vp, c_vp]),
         "muon_fp8_quantize_rows": (c_int, [c_vp, c_i64, c_i32, c_vp, c_vp, c_i32, c_i64, c_vp,
-                                           c_vp, c_vp]),
+                                           c_vp, c_vp, c_vp]),
         "muon_fp8_quantize_blocks": (c_int, [c_vp, c_i32, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp,
                                              c_vp, c_vp, c_vp]),
         "muon_fp8_quantize_cols": (c_int, [c_vp, c_i64, c_i32, c_vp, c_i32, c_vp, c_i64, c_vp,
@@ -543,9 +543,12 @@ def muon_moe_combine_backward(handle: int, grad_out, y, pos, weights, grad_y, gr
         _stream_of(stream, grad_out)))
 
 
-def muon_fp8_quantize_rows(handle: int, x, q, scales, pos=None, stream=None) -> None:
+def muon_fp8_quantize_rows(handle: int, x, q, scales, pos=None, offsets=None,
+                           stream=None) -> None:
     """Rows of ``x`` [tokens, hidden] (BF16) to e4m3 ``q`` with a scale byte
-    (E8M0) per 128; with ``pos`` [tokens, k], row t goes to rows pos[t]."""
+    (E8M0) per 128; with ``pos`` [tokens, k], row t goes to rows pos[t].  With
+    ``offsets`` (muon_moe_plan's) only the rows of some expert, the first
+    offsets[-1], are read and written."""
     (t, d), r = x.shape, q.shape[0]
     k = 0
     if pos is not None:
@@ -554,8 +557,9 @@ def muon_fp8_quantize_rows(handle: int, x, q, scales, pos=None, stream=None) -> 
         raise ValueError(f"q must have {t} rows, got {r}")
     _check(load_library().muon_fp8_quantize_rows(
         handle, t, d, _want("x", x, (t, d), "bf16"),
-        0 if pos is None else _want("pos", pos, (t, k), "i32"), k, r, _want("q", q, (r, d), "e4m3"),
-        _want("scales", scales, (r, _nb(d)), "e8m0"), _stream_of(stream, x)))
+        0 if pos is None else _want("pos", pos, (t, k), "i32"), k, r,
+        0 if offsets is None else _want("offsets", offsets, offsets.shape, "i32") + 4 * (offsets.numel() - 1),
+        _want("q", q, (r, d), "e4m3"), _want("scales", scales, (r, _nb(d)), "e8m0"), _stream_of(stream, x)))
 
 
 def muon_fp8_quantize_blocks(handle: int, w, q=None, scales=None, qt=None, scales_t=None,

@@ -102,10 +102,11 @@ constexpr int kRowThreads = 256;
 
 __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(
     const uint16_t* __restrict__ x, int64_t tokens, int d, int blocks,
-    const int32_t* __restrict__ pos, int k, int64_t rows, uint8_t* __restrict__ q,
-    uint8_t* __restrict__ scales, int* err) {
+    const int32_t* __restrict__ pos, int k, int64_t rows, const int32_t* __restrict__ live_rows,
+    uint8_t* __restrict__ q, uint8_t* __restrict__ scales, int* err) {
   grid_dep_wait();
   grid_dep_launch();
+  if (live_rows != nullptr) tokens = min(tokens, static_cast<int64_t>(*live_rows));
   const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x) >> 4;
   const int sub = threadIdx.x & 15;
   const int64_t t = unit / blocks;
@@ -446,12 +447,12 @@ __global__ void __launch_bounds__(kTileThreads, 3) quantize_cols_kernel(
 }  // namespace
 
 cudaError_t launch_fp8_quantize_rows(const uint16_t* x, int64_t tokens, int d, const int32_t* pos,
-                                     int k, int64_t rows, uint8_t* q, uint8_t* scales, int* err,
-                                     cudaStream_t s) {
+                                     int k, int64_t rows, const int32_t* live, uint8_t* q,
+                                     uint8_t* scales, int* err, cudaStream_t s) {
   const int blocks = (d + kFp8Block - 1) / kFp8Block;
   const int64_t grid = (tokens * blocks * 16 + kRowThreads - 1) / kRowThreads;
   return launch_pdl(quantize_rows_kernel, dim3(static_cast<unsigned>(grid)), dim3(kRowThreads), 0, s,
-                    x, tokens, d, blocks, pos, k, rows, q, scales, err);
+                    x, tokens, d, blocks, pos, k, rows, live, q, scales, err);
 }
 
 cudaError_t launch_fp8_quantize_blocks(const void* w, bool bf16, int experts, int n, int k,

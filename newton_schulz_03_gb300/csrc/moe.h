@@ -62,10 +62,11 @@ cudaError_t fp8_gemm_init();
 constexpr int kFp8Block = 128;   // values that share one scale
 
 // x [tokens][d] BF16 -> q e4m3, scales E8M0 [.][ceil(d/128)].  pos NULL:
-// row t goes to row t; else to every row pos[t][j] >= 0 (of `rows`).
+// row t goes to row t; else to every row pos[t][j] >= 0 (of `rows`).  live:
+// NULL, or how many rows of x there are.
 cudaError_t launch_fp8_quantize_rows(const uint16_t* x, int64_t tokens, int d, const int32_t* pos,
-                                     int k, int64_t rows, uint8_t* q, uint8_t* scales, int* err,
-                                     cudaStream_t s);
+                                     int k, int64_t rows, const int32_t* live, uint8_t* q,
+                                     uint8_t* scales, int* err, cudaStream_t s);
 
 // w [experts][n][k], FP32 or BF16 -> q [experts][n][k] and qt
 // [experts][k][n] with one scale per 128 x 128 block; either output may be NULL.

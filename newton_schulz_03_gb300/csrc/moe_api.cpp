@@ -271,7 +271,8 @@ muon_status_t muon_moe_combine_backward(muon_handle_t h, int64_t tokens, int32_t
 
 muon_status_t muon_fp8_quantize_rows(muon_handle_t h, int64_t tokens, int32_t hidden,
                                      const uint16_t* x, const int32_t* pos, int32_t top_k,
-                                     int64_t rows, uint8_t* q, uint8_t* scales, void* stream) {
+                                     int64_t rows, const int32_t* live_rows, uint8_t* q,
+                                     uint8_t* scales, void* stream) {
   muon::HandleInfo hi;
   MUON_TRY(info_of(h, &hi));
   MUON_TRY(check_hidden("hidden", hidden));
@@ -292,8 +293,8 @@ muon_status_t muon_fp8_quantize_rows(muon_handle_t h, int64_t tokens, int32_t hi
                              {scales, rows * blocks_of(hidden), true}}));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   muon::LaunchMark mark(h, MUON_KERNEL_FP8_QUANTIZE, s);
-  return launched(muon::launch_fp8_quantize_rows(x, tokens, hidden, pos, top_k, rows, q, scales,
-                                                 hi.dev_err, s),
+  return launched(muon::launch_fp8_quantize_rows(x, tokens, hidden, pos, top_k, rows, live_rows, q,
+                                                 scales, hi.dev_err, s),
                   "row quantiser");
 }
 

@@ -58,6 +58,20 @@ def test_rows(ns, h, rows, d):
     ns.muon_last_device_error(h)
 
 
+def test_rows_past_the_last_expert_are_left_alone(ns, h):
+    x = values(40, 272, 9)
+    x[25:] = float("nan")
+    off = torch.tensor([0, 3, 25], dtype=torch.int32, device="cuda")
+    q = torch.full((40, 272), 9.0, device="cuda").to(F8)
+    s = torch.full((40, 3), 200, dtype=torch.uint8, device="cuda")
+    ns.muon_fp8_quantize_rows(h, x, q, s, offsets=off)
+    ns.muon_last_device_error(h)
+    want, ws = ref.quantize_rows(host(x[:25]))
+    np.testing.assert_array_equal(q_of(q)[:25], want)
+    np.testing.assert_array_equal(s.cpu().numpy()[:25], ws)
+    assert (q_of(q)[25:] == 9.0).all() and (s[25:] == 200).all()
+
+
 @pytest.mark.parametrize("t,k,d", [(9, 3, 272), (1, 7, 4096), (65, 2, 16)])
 def test_rows_sent_to_experts(ns, h, t, k, d):
     x = values(t, d, t)

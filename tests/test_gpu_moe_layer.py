@@ -91,3 +91,68 @@ def test_one_token_and_many_agree(example):
             one, _ = layer.forward(x[t:t + 1].contiguous())
             # The router's FP32 product may add up in another order.
             assert rel(one[0].double().cpu().numpy(), many[t].double().cpu().numpy()) <= 2.0**-8
+
+
+def test_padding_tokens_change_nothing(example):
+    """Masked tokens get zeros, leave every gradient as it was, and the rows
+    that no expert has may hold anything."""
+    ns = example.ns
+    with ns.Handle() as h:
+        layer = example.ExpertLayer(h.value, hidden=256, intermediate=128, experts=16, top_k=4, seed=6)
+        x = torch.randn(50, 256, device="cuda").bfloat16()
+        grad = torch.randn(50, 256, device="cuda").bfloat16()
+        y, saved = layer.forward(x)
+        gx = layer.backward(grad, saved)
+        want = [g.clone() for g in layer.grads]
+        # The same tokens with 14 padding tokens behind them; freed memory full of NaN.
+        px = torch.cat([x, torch.full((14, 256), float("nan"), device="cuda", dtype=torch.bfloat16)])
+        px[50:] = 1.0
+        pg = torch.cat([grad, torch.zeros(14, 256, device="cuda", dtype=torch.bfloat16)])
+        junk = [torch.full((64 * 4 * 256,), float("nan"), device="cuda", dtype=torch.bfloat16) for _ in range(12)]
+        del junk
+        mask = (torch.arange(64, device="cuda") < 50).to(torch.uint8)
+        py, psaved = layer.forward(px, mask)
+        pgx = layer.backward(pg, psaved)
+        ns.muon_last_device_error(h.value)
+        assert torch.equal(py[50:], torch.zeros_like(py[50:]))
+        assert torch.equal(py[:50], y) and torch.equal(pgx[:50], gx)
+        assert torch.equal(layer.grads[0], want[0]) and torch.equal(layer.grads[1], want[1])
+
+
+def test_in_a_graph(example):
+    """The serving path captured and replayed on new input gives what eager calls give."""
+    ns = example.ns
+    with ns.Handle() as h:
+        layer = example.ExpertLayer(h.value, hidden=256, intermediate=128, experts=16, top_k=4, seed=7)
+        x = torch.randn(2000, 256, device="cuda").bfloat16()
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            layer.forward(x)                 # grows the workspace, warms the router's product
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            y, _ = layer.forward(x)
+        for seed in (1, 2):
+            x.copy_(torch.randn(2000, 256, generator=torch.Generator("cuda").manual_seed(seed), device="cuda").bfloat16())
+            graph.replay()
+            torch.cuda.synchronize()
+            want, _ = layer.forward(x)
+            # The router's FP32 product may run another kernel under capture.
+            assert rel(y.double().cpu().numpy(), want.double().cpu().numpy()) <= 2.0**-7
+        ns.muon_last_device_error(h.value)
+
+
+def test_launches_are_counted(example):
+    ns = example.ns
+    with ns.Handle() as h:
+        layer = example.ExpertLayer(h.value, hidden=64, intermediate=32, experts=4, top_k=2)
+        x = torch.randn(9, 64, device="cuda").bfloat16()
+        ns.muon_reset_kernel_stats(h.value)
+        ns.muon_set_kernel_timing(h.value, True)
+        y, saved = layer.forward(x)
+        layer.backward(y, saved)
+        ns.muon_set_kernel_timing(h.value, False)
+        st = ns.muon_kernel_stats(h.value)
+        want = dict(moe_route=2, moe_plan=1, moe_combine=3, fp8_quantize=8, fp8_product=4, fp8_wgrad=2)
+        assert {k: st["launches"][k] for k in want} == want
+        assert all(st["total_ms"][k] > 0 for k in want)
