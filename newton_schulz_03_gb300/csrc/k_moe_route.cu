@@ -601,9 +601,12 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const Route
       const float s = id >= 0 ? sigmoid(xj) : 0.f;
       const float ds = id >= 0 ? s * sigmoid(-xj) : 0.f;
       if (a.renorm) {
+        // Through the weights: a single choice's is exactly 1, and its
+        // gradient exactly 0.
         const float sum = warp_sum(s);
-        const float dot = warp_sum(id >= 0 ? g * s : 0.f);
-        dx = sum > 0.f ? (g - dot / sum) / sum * ds : 0.f;
+        const float share = sum > 0.f ? s / sum : 0.f;
+        const float dot = warp_sum(id >= 0 ? g * share : 0.f);
+        dx = sum > 0.f ? (g - dot) / sum * ds : 0.f;
       } else {
         dx = g * ds;
       }

@@ -174,6 +174,19 @@ def test_route_backward(ns, h, dtype, softmax, renorm, t, e, k):
     ns.muon_last_device_error(h)
 
 
+@pytest.mark.parametrize("softmax", [False, True])
+def test_a_single_renormalised_choice_has_no_gradient(ns, h, softmax):
+    """Its weight is `scale` whatever the logits are."""
+    x = torch.randn(500, 64, device="cuda") * 3
+    for k in (1, 3):
+        ids = torch.full((500, k), -1, dtype=torch.int32, device="cuda")
+        ids[:, k - 1] = torch.randint(0, 64, (500,), dtype=torch.int32, device="cuda")
+        out = torch.full_like(x, float("nan"))
+        ns.muon_moe_route_backward(h, x, ids, torch.randn(500, k, device="cuda"), out,
+                                   score=ns.SCORE_SOFTMAX if softmax else ns.SCORE_SIGMOID, scale=1.5)
+        assert (out == 0).all()
+
+
 def test_backward_of_a_bad_id_is_reported(ns, h):
     x = torch.randn(2, 16, device="cuda")
     ids = torch.tensor([[0, 16], [3, -2]], dtype=torch.int32, device="cuda")
