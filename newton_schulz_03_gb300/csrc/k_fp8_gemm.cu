@@ -24,8 +24,8 @@
 // are counted from the tile's first K block, so rows need no alignment.
 //
 // A persistent pair walks the tiles.  Warp 0: TMA producer.  Warp 1: TMEM and,
-// in the even CTA, the MMAs.  Warps 2-5: epilogue, overlapped with the next
-// tile through the second accumulator.  Warps 6-7: scales.  The experts' rows
+// in the even CTA, the MMAs.  Then the epilogue's warps, overlapped with
+// the next tile through the second accumulator, and the scales'.  The experts' rows
 // are read from `offsets` on the device: every block sums the experts' tile
 // counts before its first tile, so a call needs no host copy of the routing.
 #include <cuda.h>
@@ -42,14 +42,11 @@
 namespace muon {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kEpiWarps = 4;
 constexpr int kTileM = 256;                       // pair tile: output rows of w / dw
 constexpr int kHalfM = 128;
 constexpr int kBK = 128;                          // K block: one 128-byte swizzle row, one scale
 constexpr int kABytes = kHalfM * kBK;             // 16 KB per CTA and stage
 constexpr int kSetBlocks = 4;                     // K blocks per set of scales
-constexpr int kSets = 4;                          // sets in the ring
 constexpr int kScaleBytes = 512 + 1024;           // per set: 128 A cells, 256 B cells
 constexpr int kMaxTokens = 224;                   // rows: widest token tile
 constexpr int kWidthUnit = 32;                    // MMA columns come in multiples of this
@@ -61,6 +58,13 @@ constexpr int kMaps = kMaxTokens / kWidthUnit;    // B boxes: half a width each
 
 template <bool GRAD>
 struct Layout {
+  // Epilogue warps: a multiple of four, each quarter of the accumulator's lanes
+  // shared by kEpiWarps / 4 of them.  Rows: tiles with few K blocks are bound by
+  // the epilogue.  Weight gradient: four with more staging each are faster.
+  static constexpr int kEpiWarps = 4;
+  static constexpr int kScaleWarps = GRAD ? 2 : 4;
+  static constexpr int kSets = GRAD ? 4 : 8;                  // sets of scales in the ring
+  static constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
   static constexpr int kAccCols = GRAD ? kGradN : kMaxTokens;
   static constexpr int kStages = GRAD ? 4 : 6;                // operand stages
   static constexpr int kOutBufs = GRAD ? 4 : 2;               // per epilogue warp
@@ -72,7 +76,7 @@ struct Layout {
   static constexpr int kTableAt = kOutAt + kEpiWarps * kOutBufs * kOutBuf;
   static constexpr int kTableBytes = (kMoeMaxExperts + 4) * 4;
   static constexpr int kBarAt = kTableAt + 2 * kTableBytes;
-  static constexpr int kSmem = kBarAt + 256 + 1024;
+  static constexpr int kSmem = kBarAt + 384 + 1024;
   static_assert(kBBytes % 1024 == 0 && kOutAt % 1024 == 0, "swizzle atoms");
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
@@ -156,16 +160,17 @@ __device__ __forceinline__ bool decode(const Fp8Args& p, const int32_t* first, c
   return true;
 }
 
-// Fills first[] and start[] (256 threads, 4 experts each).
+// Fills first[] and start[] (all threads, a few experts each).
 template <bool GRAD>
 __device__ __forceinline__ void scan_experts(const Fp8Args& p, int32_t* first, int32_t* start,
                                              int32_t* warp_total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int count[4], sum = 0;
+  constexpr int kPer = kMoeMaxExperts / Layout<GRAD>::kThreads + 1;   // and the end of the last
+  int count[kPer], sum = 0;
   bool bad = false;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = threadIdx.x * 4 + i;
+  for (int i = 0; i < kPer; ++i) {
+    const int e = threadIdx.x * kPer + i;
     count[i] = 0;
     if (e < p.experts) {
       const int a = p.offsets[e], b = p.offsets[e + 1];
@@ -196,17 +201,13 @@ __device__ __forceinline__ void scan_experts(const Fp8Args& p, int32_t* first, i
   for (int i = 0; i < warp; ++i) at += warp_total[i];
   const int limit = GRAD ? static_cast<int>(p.rows / kBK) : INT32_MAX;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = threadIdx.x * 4 + i;
+  for (int i = 0; i < kPer; ++i) {
+    const int e = threadIdx.x * kPer + i;
     if (e <= p.experts) {
       bad = bad || at > limit;
       first[e] = min(at, limit);
     }
     at += count[i];
-  }
-  if (threadIdx.x == kThreads - 1 && p.experts == 4 * kThreads) {
-    bad = bad || at > limit;
-    first[p.experts] = min(at, limit);
   }
   if (bad && blockIdx.x == 0) atomicOr(p.err, kDevErrIndex);
 }
@@ -235,11 +236,14 @@ struct SetCursor {
       live = decode<GRAD>(p, first, start, t, o);
     }
   }
+  // `sets` sets further.
   template <bool GRAD>
-  __device__ __forceinline__ void next(const Fp8Args& p, const int32_t* first, const int32_t* start,
-                                       int step) {
-    kb += kSetBlocks;
-    settle<GRAD>(p, first, start, step);
+  __device__ __forceinline__ void advance(const Fp8Args& p, const int32_t* first,
+                                          const int32_t* start, int step, int sets) {
+    for (int i = 0; i < sets && live; ++i) {
+      kb += kSetBlocks;
+      settle<GRAD>(p, first, start, step);
+    }
   }
 };
 
@@ -302,10 +306,11 @@ __device__ __forceinline__ void load_set(const Fp8Args& p, const SetCursor& s, u
 }
 
 template <bool GRAD>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThreads, 1)
     fp8_product_kernel(const __grid_constant__ Maps maps, const Fp8Args p) {
   using L = Layout<GRAD>;
-  constexpr int kStages = L::kStages;
+  constexpr int kStages = L::kStages, kSets = L::kSets;
+  constexpr int kEpiWarps = L::kEpiWarps, kScaleWarps = L::kScaleWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -525,7 +530,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                              static_cast<uint32_t>(acc * L::kAccCols);
-      for (int cb = 0; cb * 32 < o.cols; ++cb) {
+      for (int cb = (warp - 2) >> 2; cb * 32 < o.cols; cb += kEpiWarps / 4) {
         uint32_t v[32];
         __syncwarp();
         if (!empty_sum) {
@@ -558,20 +563,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ptx::bulk_commit();
           }
         } else {
-          // A lane holds one output column of 32 tokens: turned in shared
-          // memory into 64 bytes per token, rounded once to BF16.
+          // A lane holds one output column of 32 tokens.  Two tokens' values
+          // rounded to BF16 make a word (half the stores to shared memory, which
+          // bound tiles with few K blocks); a lane then takes the words of eight
+          // columns, and halves of them are 16 bytes of either token.  Odd pairs'
+          // words are stored four places round, so that both halves' reads hit
+          // all banks.
+          uint32_t* words = reinterpret_cast<uint32_t*>(buf);
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            *reinterpret_cast<__nv_bfloat16*>(buf + j * 64 + lane * 2) =
-                __float2bfloat16_rn(__uint_as_float(v[j]));
+          for (int q = 0; q < 16; ++q) {
+            const __nv_bfloat162 two =
+                __floats2bfloat162_rn(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
+            words[q * 32 + (lane ^ ((q & 1) << 2))] = *reinterpret_cast<const uint32_t*>(&two);
+          }
           __syncwarp();
-          const int n = row0 + (lane & 3) * 8;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int tok = i * 8 + (lane >> 2);
-            if (cb * 32 + tok < o.cols && n < p.n)
-              *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(o.c0 + cb * 32 + tok) * p.n + n) =
-                  *reinterpret_cast<const uint4*>(buf + tok * 64 + (lane & 3) * 16);
+          for (int i = 0; i < 2; ++i) {
+            const int pr = i * 8 + (lane >> 2), g = lane & 3;
+            const int at = pr * 32 + ((g * 8) ^ ((pr & 1) << 2));
+            const uint4 lo = *reinterpret_cast<const uint4*>(words + at);
+            const uint4 hi = *reinterpret_cast<const uint4*>(words + (at ^ 4));
+            const int tok = cb * 32 + 2 * pr, n = row0 + g * 8;
+            __nv_bfloat16* to = p.y + static_cast<int64_t>(o.c0 + tok) * p.n + n;
+            if (tok < o.cols && n < p.n)
+              *reinterpret_cast<uint4*>(to) =
+                  make_uint4(__byte_perm(lo.x, lo.y, 0x5410), __byte_perm(lo.z, lo.w, 0x5410),
+                             __byte_perm(hi.x, hi.y, 0x5410), __byte_perm(hi.z, hi.w, 0x5410));
+            if (tok + 1 < o.cols && n < p.n)
+              *reinterpret_cast<uint4*>(to + p.n) =
+                  make_uint4(__byte_perm(lo.x, lo.y, 0x7632), __byte_perm(lo.z, lo.w, 0x7632),
+                             __byte_perm(hi.x, hi.y, 0x7632), __byte_perm(hi.z, hi.w, 0x7632));
           }
         }
       }
@@ -588,22 +609,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ scales (both CTAs)
-    // Warp `which` fills the sets which, which + 2, ...; a set's loads are in
-    // flight while it waits for its place.  They follow the arrival for the set
-    // before: a release waits for its thread's loads too.
+    // Warp `which` fills the sets which, which + kScaleWarps, ...; a set's loads
+    // are in flight while it waits for its place.  They follow the arrival for
+    // the set before: a release waits for its thread's loads too.  A set takes a
+    // warp some 2500 cycles (loads, proxy fence, release): four warps keep up
+    // with tiles of a few K blocks.
     const int which = warp - 2 - kEpiWarps;
     SetCursor at{};
     at.begin<GRAD>(p, first, start, pair);
     at.settle<GRAD>(p, first, start, npairs);
-    if (which == 1 && at.live) at.next<GRAD>(p, first, start, npairs);
+    at.advance<GRAD>(p, first, start, npairs, which);
     int set = which;
     uint32_t set_phase = 0;
     bool ok = true;
     while (at.live) {
       uint32_t cells[12];
       load_set<GRAD>(p, at, rank, lane, cells);
-      at.next<GRAD>(p, first, start, npairs);
-      if (at.live) at.next<GRAD>(p, first, start, npairs);
+      at.advance<GRAD>(p, first, start, npairs, kScaleWarps);
       const bool got = ptx::mbar_wait_cluster(&set_empty[set], set_phase ^ 1u, abort_flag);
       if (!__all_sync(0xffffffffu, got)) {
         ok = false;
@@ -617,7 +639,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&set_full[set]), 0));
-      set += 2;
+      set += kScaleWarps;
       if (set >= kSets) {
         set -= kSets;
         set_phase ^= 1u;
@@ -668,7 +690,7 @@ cudaError_t launch(const Maps& maps, const Fp8Args& p, int64_t max_tiles, int nu
   if (resident == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(Layout<GRAD>::kThreads, 1, 1);
     cfg.dynamicSmemBytes = Layout<GRAD>::kSmem;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, fp8_product_kernel<GRAD>, &cfg) != cudaSuccess || n < 1) {
@@ -682,7 +704,8 @@ cudaError_t launch(const Maps& maps, const Fp8Args& p, int64_t max_tiles, int nu
   if (pairs > max_tiles) pairs = max_tiles;
   if (pairs < 1) pairs = 1;
   if (max_tiles + 2 * pairs >= INT32_MAX) return cudaErrorInvalidValue;   // tile numbers are 32 bits
-  return launch_pdl(fp8_product_kernel<GRAD>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads),
+  return launch_pdl(fp8_product_kernel<GRAD>, dim3(static_cast<unsigned>(2 * pairs)),
+                    dim3(Layout<GRAD>::kThreads),
                     Layout<GRAD>::kSmem, s, maps, p);
 }
 
