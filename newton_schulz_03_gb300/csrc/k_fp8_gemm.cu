@@ -66,8 +66,8 @@ struct Layout {
   static constexpr int kSets = GRAD ? 4 : 8;                  // sets of scales in the ring
   static constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
   static constexpr int kAccCols = GRAD ? kGradN : kMaxTokens;
-  static constexpr int kStages = GRAD ? 4 : 6;                // operand stages
-  static constexpr int kOutBufs = GRAD ? 4 : 2;               // per epilogue warp
+  static constexpr int kStages = GRAD ? 5 : 6;                // operand stages, at most
+  static constexpr int kOutBufs = 2;                          // per epilogue warp
   static constexpr int kBBytes = (kAccCols / 2) * kBK;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kOutBuf = GRAD ? 4096 : 2048;          // one 32 x 32 chunk
@@ -92,6 +92,7 @@ struct Fp8Args {
   int32_t n_blocks, k_blocks;
   int32_t tiles_m, tiles_n;
   __nv_bfloat16* y;
+  int32_t stages;       // operand stages in use
   int32_t accumulate;
   int* err;
 };
@@ -247,61 +248,72 @@ struct SetCursor {
   }
 };
 
-// A row's scale bytes of K blocks kb .. kb + 3 (below `end`), byte 0 first.
-__device__ __forceinline__ uint32_t four_along(const uint8_t* row, int kb, int end, bool words) {
-  if (words) return __ldg(reinterpret_cast<const uint32_t*>(row + kb));
-  uint32_t v = 0u;
+// Scale bytes of n K blocks (1..4, `step` apart) for C rows at offsets off[] of
+// `base`, as the rows' cells, byte 0 first.  Only the loads that are needed, all
+// in flight together, with one 32-bit offset per row: a warp by itself takes
+// these at the pace of its instructions.
+template <int C>
+__device__ __forceinline__ void load_cells(const uint8_t* __restrict__ base, int64_t step, int n,
+                                           const uint32_t (&off)[C], uint32_t* cells) {
+  uint32_t raw[kSetBlocks][C];
 #pragma unroll
-  for (int i = 0; i < kSetBlocks; ++i)
-    if (kb + i < end) v |= static_cast<uint32_t>(__ldg(row + kb + i)) << (8 * i);
-  return v;
+  for (int i = 0; i < kSetBlocks; ++i) {
+    if (i < n) {
+      const uint8_t* at = base + i * step;
+#pragma unroll
+      for (int c = 0; c < C; ++c) raw[i][c] = __ldg(at + off[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < C; ++c) raw[i][c] = 0u;
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    cells[c] = raw[0][c] | (raw[1][c] << 8) | (raw[2][c] << 16) | (raw[3][c] << 24);
 }
 
-__device__ __forceinline__ uint32_t four_across(const uint8_t* at, int64_t pitch, int n) {
-  uint32_t v = 0u;
-#pragma unroll
-  for (int i = 0; i < kSetBlocks; ++i)
-    if (i < n) v |= static_cast<uint32_t>(__ldg(at + i * pitch)) << (8 * i);
-  return v;
-}
+// This lane's cells of one set: rows lane + 32 i, four of A's, seven of B's.
+// Rows past the tile's or the matrix's read its last one's scales: they touch
+// no result that is written.
+constexpr int kCells = 4 + kMaxTokens / 32;
+static_assert(kGradN <= kMaxTokens && kMaxTokens <= 256, "B's cells");
 
-// This lane's cells of one set: rows lane + 32 i, four of A's, eight of B's.
 template <bool GRAD>
 __device__ __forceinline__ void load_set(const Fp8Args& p, const SetCursor& s, uint32_t rank,
-                                         int lane, uint32_t (&cells)[12]) {
+                                         int lane, uint32_t (&cells)[kCells]) {
   const Tile& o = s.o;
   const int row_a = o.n0 + static_cast<int>(rank) * kHalfM;
+  const int n = min(kSetBlocks, o.nkb - s.kb);
+  constexpr int kB = kCells - 4;
+  uint32_t off[kB];
   if (GRAD) {
     const int64_t kb = o.kb0 + s.kb;
-    const int n = o.nkb - s.kb;
+    uint32_t off_a[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = row_a + i * 32 + lane;
-      cells[i] = r < p.n ? four_across(p.a_scales + kb * p.n + r, p.n, n) : 0u;
-    }
+    for (int i = 0; i < 4; ++i) off_a[i] = min(row_a + i * 32 + lane, p.n - 1);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = o.c0 + i * 32 + lane;
-      cells[4 + i] = i * 32 < kGradN && c < p.k ? four_across(p.b_scales + kb * p.k + c, p.k, n) : 0u;
-    }
+    for (int i = 0; i < kB; ++i) off[i] = min(o.c0 + i * 32 + lane, p.k - 1);
+    load_cells<4>(p.a_scales + kb * p.n, p.n, n, off_a, cells);
+    load_cells<kB>(p.b_scales + kb * p.k, p.k, n, off, cells + 4);
   } else {
-    // Rows of a multiple of four blocks start on a word: the buffers are
-    // 16-byte aligned.
-    const bool words = p.k_blocks % kSetBlocks == 0;
-    uint32_t w = 0u;
-    if (row_a < p.n)
-      w = four_along(p.a_scales + (static_cast<int64_t>(o.expert) * p.n_blocks + row_a / kBK) * p.k_blocks,
-                     s.kb, o.nkb, words);
+    const uint8_t* a = p.a_scales + s.kb + (static_cast<int64_t>(o.expert) * p.n_blocks +
+                                            min(row_a / kBK, p.n_blocks - 1)) * p.k_blocks;
+    const uint8_t* b = p.b_scales + s.kb + static_cast<int64_t>(o.c0) * p.k_blocks;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) cells[i] = w;
+    for (int i = 0; i < kB; ++i) off[i] = min(i * 32 + lane, o.cols - 1) * p.k_blocks;
+    // Rows of a multiple of four blocks start on a word (the buffers are
+    // 16-byte aligned): one load per row.
+    if (p.k_blocks % kSetBlocks == 0) {
+      cells[0] = __ldg(reinterpret_cast<const uint32_t*>(a));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = i * 32 + lane;
-      cells[4 + i] = 0u;
-      if (c < o.cols)
-        cells[4 + i] = four_along(p.b_scales + static_cast<int64_t>(o.c0 + c) * p.k_blocks, s.kb,
-                                  o.nkb, words);
+      for (int i = 0; i < kB; ++i) cells[4 + i] = __ldg(reinterpret_cast<const uint32_t*>(b + off[i]));
+    } else {
+      const uint32_t zero[1] = {0u};
+      load_cells<1>(a, 1, n, zero, cells);
+      load_cells<kB>(b, 1, n, off, cells + 4);
     }
+#pragma unroll
+    for (int i = 1; i < 4; ++i) cells[i] = cells[0];
   }
 }
 
@@ -310,6 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
     fp8_product_kernel(const __grid_constant__ Maps maps, const Fp8Args p) {
   using L = Layout<GRAD>;
   constexpr int kStages = L::kStages, kSets = L::kSets;
+  const int stages = p.stages;
   constexpr int kEpiWarps = L::kEpiWarps, kScaleWarps = L::kScaleWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -335,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
   const int npairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       ptx::mbar_init(&full[s], 1);
       ptx::mbar_init(&empty[s], 1);
     }
@@ -396,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
           ptx::tma_load_3d_pair(sa + kABytes, &maps.b[box], full_leader, (o.kb0 + kb) * kBK, row_b,
                                 0);
           ++issued;
-          if (++stage == kStages) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -406,10 +419,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
         *abort_flag = 1;
         atomicOr(p.err, kDevErrTimeout);
       }
-      const int pending = issued < kStages ? issued : kStages;
+      const int pending = issued < stages ? issued : stages;
       for (int j = 0; j < pending; ++j) {
         if (stage == 0) {
-          stage = kStages;
+          stage = stages;
           phase ^= 1u;
         }
         --stage;
@@ -476,7 +489,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
               ptx::tc_commit_pair_multicast(&empty[stage], 0x3);
             }
             __syncwarp();
-            if (++stage == kStages) {
+            if (++stage == stages) {
               stage = 0;
               phase ^= 1u;
             }
@@ -612,7 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
     // Warp `which` fills the sets which, which + kScaleWarps, ...; a set's loads
     // are in flight while it waits for its place.  They follow the arrival for
     // the set before: a release waits for its thread's loads too.  A set takes a
-    // warp some 2500 cycles (loads, proxy fence, release): four warps keep up
+    // warp some 3000 cycles (loads, proxy fence, release): four warps keep up
     // with tiles of a few K blocks.
     const int which = warp - 2 - kEpiWarps;
     SetCursor at{};
@@ -623,7 +636,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
     uint32_t set_phase = 0;
     bool ok = true;
     while (at.live) {
-      uint32_t cells[12];
+      uint32_t cells[kCells];
       load_set<GRAD>(p, at, rank, lane, cells);
       at.advance<GRAD>(p, first, start, npairs, kScaleWarps);
       const bool got = ptx::mbar_wait_cluster(&set_empty[set], set_phase ^ 1u, abort_flag);
@@ -635,10 +648,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
       uint4* to = reinterpret_cast<uint4*>(smem + L::kScaleAt + set * kScaleBytes);
       to[lane] = make_uint4(cells[0], cells[1], cells[2], cells[3]);
       to[32 + lane] = make_uint4(cells[4], cells[5], cells[6], cells[7]);
-      to[64 + lane] = make_uint4(cells[8], cells[9], cells[10], cells[11]);
+      to[64 + lane] = make_uint4(cells[8], cells[9], cells[10], 0u);
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&set_full[set]), 0));
+      if (lane == 0)
+        ptx::mbar_arrive_cluster_cta_release(ptx::mapa_shared(ptx::smem_addr(&set_full[set]), 0));
       set += kScaleWarps;
       if (set >= kSets) {
         set -= kSets;
@@ -742,6 +756,7 @@ cudaError_t launch_fp8_grouped_matmul(const uint8_t* x, const uint8_t* x_scales,
   p.n_blocks = (n + kBK - 1) / kBK;
   p.k_blocks = (k + kBK - 1) / kBK;
   p.tiles_m = (n + kTileM - 1) / kTileM;
+  p.stages = Layout<false>::kStages;
   p.y = reinterpret_cast<__nv_bfloat16*>(y);
   p.err = err;
   const int64_t token_tiles = (rows < experts ? rows : experts) + rows / kMaxTokens;
@@ -769,6 +784,12 @@ cudaError_t launch_fp8_grouped_wgrad(const uint8_t* yt, const uint8_t* yt_scales
   p.rows = cap;
   p.tiles_m = (n + kTileM - 1) / kTileM;
   p.tiles_n = (k + kGradN - 1) / kGradN;
+  // Few K blocks per expert: writing dw bounds the call, and pairs that load no
+  // further than the next tile stay together, so that neighbouring tiles' rows
+  // leave L2 as whole runs.  Measured with 2 / 5 stages: 2.1 blocks per expert
+  // (2048 x 8704 x 16) 184 / 200 us, 2.7 (1536 x 4096 x 128) 587 / 680 us; 5.0
+  // (1536 x 4096 x 64) 437 / 305 us, 32 (2048 x 8704 x 8) 725 / 426 us.
+  p.stages = 2 * (cap / kBK) < 7 * static_cast<int64_t>(experts) ? 2 : Layout<true>::kStages;
   p.accumulate = accumulate ? 1 : 0;
   p.err = err;
   return launch<true>(maps, p, int64_t(experts) * p.tiles_m * p.tiles_n, num_sms, s);

@@ -200,6 +200,15 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
                : "memory");
 }
 
+// Arrive on either CTA's barrier, releasing at the scope of this CTA: for
+// shared memory that this CTA's own tensor core is to read (the arrival follows
+// a proxy fence); nothing of it is read by the other CTA's threads.  A release
+// at cluster scope waits for every store of the SM in flight.
+__device__ __forceinline__ void mbar_arrive_cluster_cta_release(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar_addr, uint32_t parity) {
   uint32_t done;
   asm volatile(
