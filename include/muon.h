@@ -531,13 +531,15 @@ muon_status_t muon_fp8_quantize_blocks(muon_handle_t handle, int32_t experts, in
                                        uint8_t* qt, uint8_t* scales_t, void* stream);
 
 /* Columns of each expert's rows, for the weight gradient, whose sums run
- * over rows: blocks of 128 rows of one expert (the last filled with zeros),
- * written transposed.  An expert's columns of qt [hidden][capacity] start at
- * 128 times the sum of ceil(rows / 128) over the experts before it; scales:
- * [capacity / 128][hidden].  capacity is a multiple of 128; rows + 127
- * experts, rounded down to one, always suffices.  Columns past the last
- * expert's are not written.  Row r is x[r] of x [x_rows][hidden] (BF16), or
- * x[slots[r] / top_k] with slots [rows] from muon_moe_plan. */
+ * over rows: blocks of 128 rows of one expert, written transposed.  An
+ * expert's columns of qt [hidden][capacity] start at 128 times the sum of
+ * ceil(rows / 128) over the experts before it; they hold its rows, then zeros
+ * to the next multiple of 32, and what is left of its last 128 is not written
+ * (muon_fp8_grouped_wgrad does not use it), nor are columns past the last
+ * expert's.  scales: [capacity / 128][hidden].  capacity is a multiple of
+ * 128; rows + 127 experts, rounded down to one, always suffices.  Row r is
+ * x[r] of x [x_rows][hidden] (BF16), or x[slots[r] / top_k] with slots [rows]
+ * from muon_moe_plan. */
 muon_status_t muon_fp8_quantize_cols(muon_handle_t handle, int64_t x_rows, int32_t hidden,
                                      const uint16_t* x, int32_t experts, const int32_t* offsets,
                                      int64_t rows, const int32_t* slots, int32_t top_k, uint8_t* qt,

@@ -110,10 +110,11 @@ struct Tile {
   int cols;             // tokens or columns that exist
   int width;            // MMA columns (a multiple of kWidthUnit)
   int kb0, nkb;         // K blocks
+  int last;             // K steps of 32 in the last one
 };
 
 // first[e]: token tiles (rows) or row blocks (wgrad) before expert e;
-// start[e]: its first row.
+// start[e]: its first row (rows) or how many rows it has (wgrad).
 template <bool GRAD>
 __device__ __forceinline__ bool decode(const Fp8Args& p, const int32_t* first, const int32_t* start,
                                        uint32_t t, Tile& o) {
@@ -132,6 +133,8 @@ __device__ __forceinline__ bool decode(const Fp8Args& p, const int32_t* first, c
     o.width = kGradN;
     o.kb0 = first[o.expert];
     o.nkb = first[o.expert + 1] - o.kb0;
+    // Columns past the next multiple of 32 rows were never written.
+    o.last = min(4, (start[o.expert] - (o.nkb - 1) * kBK + 31) / 32);
     return true;
   }
   if (t >= first[p.experts] * tiles_m) return false;
@@ -158,6 +161,7 @@ __device__ __forceinline__ bool decode(const Fp8Args& p, const int32_t* first, c
   o.cols = min(o.width, m - i * o.width);
   o.kb0 = 0;
   o.nkb = p.k_blocks;
+  o.last = (p.k - (o.nkb - 1) * kBK + 31) / 32;
   return true;
 }
 
@@ -177,6 +181,7 @@ __device__ __forceinline__ void scan_experts(const Fp8Args& p, int32_t* first, i
       const int a = p.offsets[e], b = p.offsets[e + 1];
       if (GRAD) {
         bad = bad || a < 0 || b < a;
+        start[e] = max(0, b - a);
         count[i] = (max(0, b - a) + kBK - 1) / kBK;
       } else {
         // Rows outside x and y are never touched, whatever offsets holds.
@@ -481,11 +486,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
             const uint32_t idesc = ptx::idesc_mxf8_byte(idesc0, b);
             const uint64_t a_desc = a_desc0 + static_cast<uint32_t>(stage * (L::kStageBytes >> 4));
             const uint64_t b_desc = a_desc + (kABytes >> 4);
+            const int steps = kb0 + b == o.nkb - 1 ? o.last : kBK / 32;
             if (ptx::elect_one()) {
 #pragma unroll
               for (int k = 0; k < kBK / 32; ++k)
-                ptx::tc_mma_mxf8_pair(d_tmem, a_desc + k * 2, b_desc + k * 2, idesc, sa_tmem, sb_tmem,
-                                      (kb0 | b | k) != 0 ? 1u : 0u);
+                if (k < steps)
+                  ptx::tc_mma_mxf8_pair(d_tmem, a_desc + k * 2, b_desc + k * 2, idesc, sa_tmem, sb_tmem,
+                                        (kb0 | b | k) != 0 ? 1u : 0u);
               ptx::tc_commit_pair_multicast(&empty[stage], 0x3);
             }
             __syncwarp();

@@ -13,7 +13,8 @@
 //   blocks  128 x 128 of a weight matrix, as it is and transposed: the same
 //           scale serves the product with W and with its transpose
 //   cols    128 x 1 along the rows of one expert, written transposed: the
-//           operands of the weight gradient, whose sums run over rows
+//           operands of the weight gradient, whose sums run over rows (an
+//           expert's last block only as far as the next multiple of 32 rows)
 // A NaN stays NaN, an infinity becomes the largest value; both are reported
 // through the device error word.  Every kernel is bound by HBM: each value is
 // read once and written as one byte.
@@ -332,7 +333,11 @@ __global__ void __launch_bounds__(kTileThreads, 3) quantize_cols_kernel(
       if (first[mid] <= b) lo_e = mid; else hi_e = mid;
     }
     const int64_t row_end = offsets[lo_e + 1];
-    const int64_t row0 = offsets[lo_e] + static_cast<int64_t>(b - first[lo_e]) * 128 + warp * 16;
+    const int64_t block0 = offsets[lo_e] + static_cast<int64_t>(b - first[lo_e]) * 128;
+    const int64_t row0 = block0 + warp * 16;
+    // Rows of the block that are written: to the next multiple of 32, the K
+    // step of the products.  Experts with few rows are mostly padding.
+    const int width = static_cast<int>(min(int64_t(128), (row_end - block0 + 31) / 32 * 32));
 
     // Lane r of the warp looks up row r's source.
     int src = -1;
@@ -428,7 +433,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) quantize_cols_kernel(
         for (int r = 0; r < 16; ++r) words[r] = bf16_to_e4m3x4(u[r].x, u[r].y, inv01, inv23);
       }
       if (any && stripe + 1 < stripe1) load(stripe + 1);
-      put_transposed(tile, words, warp, lane);
+      if (warp * 16 < width) put_transposed(tile, words, warp, lane);
       if (warp == 0 && col < d) {
         const uint32_t bytes = static_cast<uint32_t>(ex[0] + 127) | (static_cast<uint32_t>(ex[1] + 127) << 8) |
                                (static_cast<uint32_t>(ex[2] + 127) << 16) | (static_cast<uint32_t>(ex[3] + 127) << 24);
@@ -436,7 +441,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) quantize_cols_kernel(
       }
       __syncthreads();
       write_transposed(tile, qt + static_cast<int64_t>(c0) * cap + static_cast<int64_t>(b) * 128, cap,
-                       min(128, d - c0), 128);
+                       min(128, d - c0), width);
       // No barrier here: the next stripe's writes to `tile` come after the
       // barrier that follows col_max, which every thread reaches after its
       // reads of `tile`; col_max was read before this stripe's second one.

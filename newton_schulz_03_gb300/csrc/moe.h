@@ -76,7 +76,7 @@ cudaError_t launch_fp8_quantize_blocks(const void* w, bool bf16, int experts, in
 
 // Rows [offsets[e], offsets[e+1]) of each expert, 128 at a time: qt [d][cap]
 // and scales [cap / 128][d], an expert's columns starting at a multiple of
-// 128, the columns past its rows zero.  Row r is x[r], or x[slots[r] / top_k].
+// 128, zero from its rows to the next multiple of 32 (not written past that).  Row r is x[r], or x[slots[r] / top_k].
 // `rows`: how many rows offsets may reach.
 cudaError_t launch_fp8_quantize_cols(const uint16_t* x, int64_t x_rows, int d,
                                      const int32_t* offsets, int experts, const int32_t* slots,

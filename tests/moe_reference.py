@@ -160,3 +160,13 @@ def cols_values(q, s):
 
 def padded_starts(offsets):
     return np.concatenate([[0], np.cumsum(-(-np.diff(offsets) // BLOCK))]) * BLOCK
+
+
+def written_columns(offsets):
+    """Which columns up to the last expert's end the column quantiser writes:
+    each expert's rows, and on to the next multiple of 32."""
+    starts = padded_starts(offsets)
+    out = np.zeros(starts[-1], dtype=bool)
+    for e in range(len(offsets) - 1):
+        out[starts[e]:starts[e] + -(-(offsets[e + 1] - offsets[e]) // 32) * 32] = True
+    return out

@@ -167,11 +167,13 @@ def wgrad_case(ns, counts, n, k, seed, extra=0):
     live = np.zeros(cap, dtype=bool)
     for e in range(len(counts)):
         live[starts[e]:starts[e] + counts[e]] = True
+    used = np.zeros(cap, dtype=bool)
+    used[:starts[-1]] = ref.written_columns(off)
     out = []
     for rows in (n, k):
         q = fp8((rows, cap), g)
         q.view(torch.uint8)[:, torch.from_numpy(~live).cuda()] = 0
-        q.view(torch.uint8)[:, int(starts[-1]):] = 0x7F       # past the experts: NaN, never read
+        q.view(torch.uint8)[:, torch.from_numpy(~used).cuda()] = 0x7F   # never written: NaN must reach nothing
         out += [q, scales((cap // 128, rows), g)]
     return off, starts, out
 
