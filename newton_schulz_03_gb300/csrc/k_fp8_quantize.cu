@@ -84,9 +84,12 @@ __device__ __forceinline__ uint32_t bf16_to_e4m3x4(uint32_t u, uint32_t v, uint3
   return r;
 }
 
-// Largest magnitude bits of BF16 pairs, as 16-bit integers (NaN the largest).
+// Largest magnitudes of BF16 pairs; a NaN carries through (its bits are above
+// an infinity's).
 __device__ __forceinline__ uint32_t max_mag2(uint32_t m, uint32_t u) {
-  return __vmaxu2(m, u & 0x7fff7fffu);
+  const __nv_bfloat162 v = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                       __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u)));
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // 2^-e as BF16 bits.
@@ -275,7 +278,8 @@ __global__ void __launch_bounds__(kTileThreads) quantize_blocks_kernel(
 // Magnitudes are compared as pairs of 16-bit integers and values scaled by
 // mixed-precision FMAs that take BF16 halves in place: the kernel is bound by
 // its instructions, not by memory.
-constexpr int kStripes = 4;
+constexpr int kStripes = 8;
+constexpr uint32_t kNoRow = 0xffffffffu;
 
 __global__ void __launch_bounds__(kTileThreads, 3) quantize_cols_kernel(
     const uint16_t* __restrict__ x, int64_t x_rows, int d, const int32_t* __restrict__ offsets,
@@ -283,6 +287,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) quantize_cols_kernel(
     uint8_t* __restrict__ qt, int64_t cap, uint8_t* __restrict__ scales, int* err) {
   __shared__ __align__(16) uint8_t tile[128 * 128];
   __shared__ uint2 col_max[kTileThreads / 32][32];
+  __shared__ __align__(16) uint32_t row_at[kTileThreads / 32][16];   // a warp's rows
   __shared__ int32_t first[kMoeMaxExperts + 1];   // first row block of each expert
   __shared__ int32_t warp_total[kTileThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -360,23 +365,30 @@ __global__ void __launch_bounds__(kTileThreads, 3) quantize_cols_kernel(
     uint2 u[16];
     const bool all = __all_sync(kAll, src >= 0 || lane >= 16);
     // Row starts in units of 16 values: 32 bits reach 2^36 values.
-    const uint32_t row_at = static_cast<uint32_t>(max(src, 0)) * static_cast<uint32_t>(d >> 4);
+    __syncwarp();
+    if (lane < 16)
+      row_at[warp][lane] =
+          src >= 0 ? static_cast<uint32_t>(src) * static_cast<uint32_t>(d >> 4) : kNoRow;
+    __syncwarp();
     const auto load = [&](int stripe) {
       const int col = stripe * 128 + lane * 4;
       const uint16_t* from = x + col;
+      uint32_t row[16];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const uint4 v = *reinterpret_cast<const uint4*>(&row_at[warp][g * 4]);
+        row[4 * g] = v.x; row[4 * g + 1] = v.y; row[4 * g + 2] = v.z; row[4 * g + 3] = v.w;
+      }
       if (all && stripe * 128 + 128 <= d) {
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          u[r] = __ldg(reinterpret_cast<const uint2*>(
-              from + static_cast<uint64_t>(__shfl_sync(kAll, row_at, r)) * 16));
+          u[r] = __ldg(reinterpret_cast<const uint2*>(from + static_cast<uint64_t>(row[r]) * 16));
       } else {
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const uint32_t row = __shfl_sync(kAll, row_at, r);
-          const bool there = __shfl_sync(kAll, src, r) >= 0;
           u[r] = make_uint2(0u, 0u);
-          if (there && col < d)
-            u[r] = __ldg(reinterpret_cast<const uint2*>(from + static_cast<uint64_t>(row) * 16));
+          if (row[r] != kNoRow && col < d)
+            u[r] = __ldg(reinterpret_cast<const uint2*>(from + static_cast<uint64_t>(row[r]) * 16));
         }
       }
     };
@@ -393,52 +405,55 @@ __global__ void __launch_bounds__(kTileThreads, 3) quantize_cols_kernel(
       }
       col_max[warp][lane] = m;
       __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kTileThreads / 32; ++w) {
-        const uint2 o = col_max[w][lane];
-        m.x = __vmaxu2(m.x, o.x);
-        m.y = __vmaxu2(m.y, o.y);
-      }
-      uint32_t top[4] = {m.x << 16, m.x & 0xffff0000u, m.y << 16, m.y & 0xffff0000u};
-      if (max(max(top[0], top[1]), max(top[2], top[3])) >= kInfBits) {
-        atomicOr(err, kDevErrInput);
-        // NaN takes no part in the magnitude: this warp's columns again, over
-        // all rows of the block.
-        for (int c = 0; c < 4; ++c) {
-          if (top[c] <= kInfBits) continue;
-          top[c] = 0u;
-          const int64_t r_begin = row0 - warp * 16, r_end = min(row_end, r_begin + 128);
-          for (int64_t r = max(r_begin, int64_t(0)); r < min(r_end, rows); ++r) {
-            int64_t from = r;
-            if (slots != nullptr) from = slots[r] >= 0 ? slots[r] / top_k : -1;
-            if (from < 0 || from >= x_rows || col >= d) continue;
-            const uint32_t v = static_cast<uint32_t>(x[from * d + col + c] & 0x7fffu) << 16;
-            if (v <= kInfBits) top[c] = max(top[c], v);
-          }
-        }
-      }
-      int ex[4];
-      uint32_t inv[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        ex[c] = scale_exponent(top[c]);
-        inv[c] = inverse_scale_bf16(ex[c]);
-      }
-      const uint32_t inv01 = inv[0] | (inv[1] << 16), inv23 = inv[2] | (inv[3] << 16);
       uint32_t words[16];
 #pragma unroll
       for (int r = 0; r < 16; ++r) words[r] = 0u;
-      if (any) {
+      // Warps without rows have only zeros to give (warp 0 has the scales).
+      if (any || warp == 0) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) words[r] = bf16_to_e4m3x4(u[r].x, u[r].y, inv01, inv23);
+        for (int w = 0; w < kTileThreads / 32; ++w) {
+          const uint2 o = col_max[w][lane];
+          m.x = __vmaxu2(m.x, o.x);
+          m.y = __vmaxu2(m.y, o.y);
+        }
+        uint32_t top[4] = {m.x << 16, m.x & 0xffff0000u, m.y << 16, m.y & 0xffff0000u};
+        if (max(max(top[0], top[1]), max(top[2], top[3])) >= kInfBits) {
+          atomicOr(err, kDevErrInput);
+          // NaN takes no part in the magnitude: this warp's columns again, over
+          // all rows of the block.
+          for (int c = 0; c < 4; ++c) {
+            if (top[c] <= kInfBits) continue;
+            top[c] = 0u;
+            const int64_t r_begin = row0 - warp * 16, r_end = min(row_end, r_begin + 128);
+            for (int64_t r = max(r_begin, int64_t(0)); r < min(r_end, rows); ++r) {
+              int64_t from = r;
+              if (slots != nullptr) from = slots[r] >= 0 ? slots[r] / top_k : -1;
+              if (from < 0 || from >= x_rows || col >= d) continue;
+              const uint32_t v = static_cast<uint32_t>(x[from * d + col + c] & 0x7fffu) << 16;
+              if (v <= kInfBits) top[c] = max(top[c], v);
+            }
+          }
+        }
+        int ex[4];
+        uint32_t inv[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          ex[c] = scale_exponent(top[c]);
+          inv[c] = inverse_scale_bf16(ex[c]);
+        }
+        const uint32_t inv01 = inv[0] | (inv[1] << 16), inv23 = inv[2] | (inv[3] << 16);
+        if (any) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) words[r] = bf16_to_e4m3x4(u[r].x, u[r].y, inv01, inv23);
+        }
+        if (warp == 0 && col < d) {
+          const uint32_t bytes = static_cast<uint32_t>(ex[0] + 127) | (static_cast<uint32_t>(ex[1] + 127) << 8) |
+                                 (static_cast<uint32_t>(ex[2] + 127) << 16) | (static_cast<uint32_t>(ex[3] + 127) << 24);
+          *reinterpret_cast<uint32_t*>(scales + static_cast<int64_t>(b) * d + col) = bytes;
+        }
       }
       if (any && stripe + 1 < stripe1) load(stripe + 1);
       if (warp * 16 < width) put_transposed(tile, words, warp, lane);
-      if (warp == 0 && col < d) {
-        const uint32_t bytes = static_cast<uint32_t>(ex[0] + 127) | (static_cast<uint32_t>(ex[1] + 127) << 8) |
-                               (static_cast<uint32_t>(ex[2] + 127) << 16) | (static_cast<uint32_t>(ex[3] + 127) << 24);
-        *reinterpret_cast<uint32_t*>(scales + static_cast<int64_t>(b) * d + col) = bytes;
-      }
       __syncthreads();
       write_transposed(tile, qt + static_cast<int64_t>(c0) * cap + static_cast<int64_t>(b) * 128, cap,
                        min(128, d - c0), width);
