@@ -34,10 +34,10 @@
 
 #include <cstdint>
 
+#include "fp8_ptx.cuh"
 #include "kernels.h"
 #include "launch.cuh"
 #include "moe.h"
-#include "sm103_ptx.cuh"
 
 namespace muon {
 namespace {
@@ -661,8 +661,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
       to[64 + lane] = make_uint4(cells[8], cells[9], cells[10], 0u);
       ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0)
-        ptx::mbar_arrive_cluster_cta_release(ptx::mapa_shared(ptx::smem_addr(&set_full[set]), 0));
+      if (lane == 0) {
+        if (leader)
+          ptx::mbar_arrive(&set_full[set]);
+        else
+          ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&set_full[set]), 0));
+      }
       set += kScaleWarps;
       if (set >= kSets) {
         set -= kSets;
@@ -690,10 +694,24 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// The installed driver's cuTensorMapEncodeTiled (NULL: unavailable).
+EncodeFn encoder() {
+  static const EncodeFn fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<EncodeFn>(ptr);
+  }();
+  return fn;
+}
+
 // (cols, rows, count) of bytes or FP32 values, 128-byte swizzle, zero fill.
 bool encode(CUtensorMap* map, bool fp32, const void* ptr, int64_t cols, int64_t rows, int64_t count,
             int box_cols, int box_rows) {
-  EncodeFn enc = reinterpret_cast<EncodeFn>(tensor_map_encoder());
+  const EncodeFn enc = encoder();
   if (enc == nullptr) return false;
   const cuuint64_t el = fp32 ? 4 : 1;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),

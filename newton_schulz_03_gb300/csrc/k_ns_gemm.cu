@@ -399,8 +399,6 @@ int sym_tiles_per_matrix(int tiles_m, int tiles_n) {
 
 }  // namespace
 
-void* tensor_map_encoder() { return reinterpret_cast<void*>(get_encode_fn()); }
-
 const char* ns_last_encode_error() { return g_encode_err; }
 
 // Matrices with more than 128 rows (after the transpose to wide) run on CTA

@@ -132,9 +132,6 @@ cudaError_t launch_bounded_wait_selftest(int* err, uint64_t limit_ns, cudaStream
 // Last error text of a tensor-map encode (host, thread-local).
 const char* ns_last_encode_error();
 
-// cuTensorMapEncodeTiled of the installed driver (NULL: unavailable).
-void* tensor_map_encoder();
-
 // CTA-pair (cta_group::2) variants of the three products, 256 x 256 tiles;
 // the tensor maps are built by the ns_launch_* functions above (`_t`
 // maps: 64 x 64 boxes of the same tensor, for transposed block reads).
