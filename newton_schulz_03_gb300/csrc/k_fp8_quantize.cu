@@ -101,7 +101,8 @@ __device__ __forceinline__ float lo(uint32_t u) { return __uint_as_float(u << 16
 __device__ __forceinline__ float hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
 // ------------------------------------------------------------------ rows
-// Half a warp per block of 128 values: 8 values (16 bytes) per lane.
+// Eight lanes per block of 128 values, 16 values each: a row's 16 bytes per lane
+// and store.
 constexpr int kRowThreads = 256;
 
 __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(
@@ -111,36 +112,43 @@ __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(
   grid_dep_wait();
   grid_dep_launch();
   if (live_rows != nullptr) tokens = min(tokens, static_cast<int64_t>(*live_rows));
-  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x) >> 4;
-  const int sub = threadIdx.x & 15;
+  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x) >> 3;
+  const int sub = threadIdx.x & 7;
   const int64_t t = unit / blocks;
   const int b = static_cast<int>(unit - t * blocks);
   const bool live = t < tokens;
-  const int c = b * kFp8Block + sub * 8;
+  const int c = b * kFp8Block + sub * 16;
   const bool in = live && c < d;
-  uint4 u = make_uint4(0, 0, 0, 0);
-  if (in) u = *reinterpret_cast<const uint4*>(x + t * d + c);
-  uint32_t m2 = max_mag2(max_mag2(max_mag2(u.x & 0x7fff7fffu, u.y), u.z), u.w);
+  uint4 u = make_uint4(0, 0, 0, 0), v = u;
+  if (in) {
+    const uint4* from = reinterpret_cast<const uint4*>(x + t * d + c);
+    u = from[0];
+    v = from[1];
+  }
+  const uint32_t words[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  uint32_t m2 = 0u;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(kAll, m2, o));
+  for (int i = 0; i < 8; ++i) m2 = max_mag2(m2, words[i]);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(kAll, m2, o));
   uint32_t m = max(m2 & 0xffff0000u, m2 << 16);
   if (__any_sync(kAll, m >= kInfBits)) {          // NaN takes no part in the magnitude
-    const float v[8] = {lo(u.x), hi(u.x), lo(u.y), hi(u.y), lo(u.z), hi(u.z), lo(u.w), hi(u.w)};
     bool bad = false;
     m = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, mag(v[i], bad));
+    for (int i = 0; i < 8; ++i) m = max(m, max(mag(lo(words[i]), bad), mag(hi(words[i]), bad)));
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
+    for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
     if (bad) atomicOr(err, kDevErrInput);
   }
   if (!live) return;
   const int e = scale_exponent(m);
   const uint32_t inv = inverse_scale_bf16(e) * 0x10001u;
-  const uint2 out =
-      make_uint2(bf16_to_e4m3x4(u.x, u.y, inv, inv), bf16_to_e4m3x4(u.z, u.w, inv, inv));
+  const uint4 out = make_uint4(
+      bf16_to_e4m3x4(u.x, u.y, inv, inv), bf16_to_e4m3x4(u.z, u.w, inv, inv),
+      bf16_to_e4m3x4(v.x, v.y, inv, inv), bf16_to_e4m3x4(v.z, v.w, inv, inv));
   if (pos == nullptr) {
-    if (in) *reinterpret_cast<uint2*>(q + t * d + c) = out;
+    if (in) *reinterpret_cast<uint4*>(q + t * d + c) = out;
     if (sub == 0) scales[t * blocks + b] = static_cast<uint8_t>(e + 127);
     return;
   }
@@ -150,7 +158,7 @@ __global__ void __launch_bounds__(kRowThreads) quantize_rows_kernel(
       if (r != -1) atomicOr(err, kDevErrIndex);
       continue;
     }
-    if (in) *reinterpret_cast<uint2*>(q + static_cast<int64_t>(r) * d + c) = out;
+    if (in) *reinterpret_cast<uint4*>(q + static_cast<int64_t>(r) * d + c) = out;
     if (sub == 0) scales[static_cast<int64_t>(r) * blocks + b] = static_cast<uint8_t>(e + 127);
   }
 }
@@ -470,7 +478,7 @@ cudaError_t launch_fp8_quantize_rows(const uint16_t* x, int64_t tokens, int d, c
                                      int k, int64_t rows, const int32_t* live, uint8_t* q,
                                      uint8_t* scales, int* err, cudaStream_t s) {
   const int blocks = (d + kFp8Block - 1) / kFp8Block;
-  const int64_t grid = (tokens * blocks * 16 + kRowThreads - 1) / kRowThreads;
+  const int64_t grid = (tokens * blocks * 8 + kRowThreads - 1) / kRowThreads;
   return launch_pdl(quantize_rows_kernel, dim3(static_cast<unsigned>(grid)), dim3(kRowThreads), 0, s,
                     x, tokens, d, blocks, pos, k, rows, live, q, scales, err);
 }

@@ -283,7 +283,7 @@ muon_status_t muon_fp8_quantize_rows(muon_handle_t h, int64_t tokens, int32_t hi
     MUON_TRY(check_rows(tokens));
     rows = tokens;
   }
-  const int64_t threads = tokens * blocks_of(hidden) * 16;
+  const int64_t threads = tokens * blocks_of(hidden) * 8;
   if (threads / 256 >= (int64_t(1) << 31) - 1)
     return fail(MUON_ERR_INVALID_ARG, "x is too large for one call");
   if (tokens == 0) return MUON_OK;
