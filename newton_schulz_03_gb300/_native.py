@@ -431,13 +431,14 @@ class _Kinds(dict):
 _KINDS = _Kinds()
 
 
-def _want(name: str, t, shape: tuple, kind: str) -> int:
-    """Address of a contiguous CUDA tensor of this shape and kind."""
-    if t.dtype in _KINDS[kind] and t.shape == shape and t.is_cuda and t.is_contiguous():
+def _want(name: str, t, shape: Optional[tuple], kind: str) -> int:
+    """Address of a contiguous CUDA tensor of this shape (None: any) and kind."""
+    if (t.dtype in _KINDS[kind] and (shape is None or t.shape == shape) and t.is_cuda
+            and t.is_contiguous()):
         return t.data_ptr()
     if t.dtype not in _KINDS[kind]:
         raise ValueError(f"{name} must be {' or '.join(map(str, _KINDS[kind]))}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if shape is not None and tuple(t.shape) != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -486,7 +487,7 @@ def muon_moe_route(handle: int, logits, ids, weights, score: int = SCORE_SIGMOID
     k = ids.shape[-1]
     _, opts = _route_options(score, groups, top_groups, group_top, 1 if renormalize else 0, scale)
     _check(load_library().muon_moe_route(
-        handle, t, e, k, _want("logits", logits, (t, e), "f32/bf16"), _dtype(logits),
+        handle, t, e, k, _want("logits", logits, None, "f32/bf16"), _dtype(logits),
         0 if bias is None else _want("bias", bias, (e,), "f32"),
         0 if mask is None else _want("mask", mask, (t,), "bytes"), opts,
         _want("ids", ids, (t, k), "i32"), _want("weights", weights, (t, k), "f32"),
@@ -502,7 +503,7 @@ def muon_moe_route_backward(handle: int, logits, ids, grad_weights, grad_logits,
     kind = _dtype(logits)
     _, opts = _route_options(score, 1, 1, 1, 1 if renormalize else 0, scale)
     _check(load_library().muon_moe_route_backward(
-        handle, t, e, k, _want("logits", logits, (t, e), "f32/bf16"), _dtype(logits),
+        handle, t, e, k, _want("logits", logits, None, "f32/bf16"), _dtype(logits),
         _want("ids", ids, (t, k), "i32"), _want("grad_weights", grad_weights, (t, k), "f32"),
         opts,
         _want("grad_logits", grad_logits, (t, e), "f32" if kind == 0 else "bf16"),
@@ -516,7 +517,7 @@ def muon_moe_plan(handle: int, ids, offsets, slots, pos, stream=None) -> None:
     n = ids.numel()
     e = offsets.shape[0] - 1
     _check(load_library().muon_moe_plan(
-        handle, n, e, _want("ids", ids, ids.shape, "i32"), _want("offsets", offsets, (e + 1,), "i32"),
+        handle, n, e, _want("ids", ids, None, "i32"), _want("offsets", offsets, (e + 1,), "i32"),
         _want("slots", slots, (n,), "i32"), _want("pos", pos, ids.shape, "i32"), _stream_of(stream, ids)))
 
 
@@ -524,7 +525,7 @@ def muon_moe_combine(handle: int, y, pos, weights, out, stream=None) -> None:
     """out[t] = sum over j of weights[t, j] y[pos[t, j]]; weights None: ones."""
     (r, d), (t, k) = y.shape, pos.shape
     _check(load_library().muon_moe_combine(
-        handle, t, k, r, d, _want("y", y, (r, d), "bf16"), _want("pos", pos, (t, k), "i32"),
+        handle, t, k, r, d, _want("y", y, None, "bf16"), _want("pos", pos, None, "i32"),
         0 if weights is None else _want("weights", weights, (t, k), "f32"),
         _want("out", out, (t, d), "bf16"), _stream_of(stream, y)))
 
@@ -536,7 +537,7 @@ def muon_moe_combine_backward(handle: int, grad_out, y, pos, weights, grad_y, gr
     (r, d), (t, k) = grad_y.shape, pos.shape
     _check(load_library().muon_moe_combine_backward(
         handle, t, k, r, d, _want("grad_out", grad_out, (t, d), "bf16"),
-        0 if y is None else _want("y", y, (r, d), "bf16"), _want("pos", pos, (t, k), "i32"),
+        0 if y is None else _want("y", y, (r, d), "bf16"), _want("pos", pos, None, "i32"),
         0 if weights is None else _want("weights", weights, (t, k), "f32"),
         _want("grad_y", grad_y, (r, d), "bf16"),
         0 if grad_weights is None else _want("grad_weights", grad_weights, (t, k), "f32"),
@@ -556,7 +557,7 @@ def muon_fp8_quantize_rows(handle: int, x, q, scales, pos=None, offsets=None,
     elif r != t:
         raise ValueError(f"q must have {t} rows, got {r}")
     _check(load_library().muon_fp8_quantize_rows(
-        handle, t, d, _want("x", x, (t, d), "bf16"),
+        handle, t, d, _want("x", x, None, "bf16"),
         0 if pos is None else _want("pos", pos, (t, k), "i32"), k, r,
         0 if offsets is None else _want("offsets", offsets, offsets.shape, "i32") + 4 * (offsets.numel() - 1),
         _want("q", q, (r, d), "e4m3"), _want("scales", scales, (r, _nb(d)), "e8m0"), _stream_of(stream, x)))
@@ -569,7 +570,7 @@ def muon_fp8_quantize_blocks(handle: int, w, q=None, scales=None, qt=None, scale
     (``qt``, ``scales_t``)."""
     e, n, k = w.shape
     _check(load_library().muon_fp8_quantize_blocks(
-        handle, e, n, k, _want("w", w, (e, n, k), "f32/bf16"), _dtype(w),
+        handle, e, n, k, _want("w", w, None, "f32/bf16"), _dtype(w),
         0 if q is None else _want("q", q, (e, n, k), "e4m3"),
         0 if scales is None else _want("scales", scales, (e, _nb(n), _nb(k)), "e8m0"),
         0 if qt is None else _want("qt", qt, (e, k, n), "e4m3"),
@@ -591,7 +592,7 @@ def muon_fp8_quantize_cols(handle: int, x, offsets, qt, scales, slots=None, top_
     (xr, d), e, cap = x.shape, offsets.shape[0] - 1, qt.shape[1]
     rows = xr if slots is None else slots.shape[0]
     _check(load_library().muon_fp8_quantize_cols(
-        handle, xr, d, _want("x", x, (xr, d), "bf16"), e, _want("offsets", offsets, (e + 1,), "i32"),
+        handle, xr, d, _want("x", x, None, "bf16"), e, _want("offsets", offsets, (e + 1,), "i32"),
         rows, 0 if slots is None else _want("slots", slots, (rows,), "i32"), top_k,
         _want("qt", qt, (d, cap), "e4m3"), cap, _want("scales", scales, (cap // 128, d), "e8m0"),
         _stream_of(stream, x)))
@@ -603,7 +604,7 @@ def muon_fp8_grouped_matmul(handle: int, x, x_scales, w, w_scales, offsets, y,
     expert; ``x`` [rows, k], ``w`` [experts, n, k] e4m3, ``y`` [rows, n] BF16."""
     (r, k), (e, n, _) = x.shape, w.shape
     _check(load_library().muon_fp8_grouped_matmul(
-        handle, r, e, n, k, _want("x", x, (r, k), "e4m3"),
+        handle, r, e, n, k, _want("x", x, None, "e4m3"),
         _want("x_scales", x_scales, (r, _nb(k)), "e8m0"), _want("w", w, (e, n, k), "e4m3"),
         _want("w_scales", w_scales, (e, _nb(n), _nb(k)), "e8m0"),
         _want("offsets", offsets, (e + 1,), "i32"), _want("y", y, (r, n), "bf16"), _stream_of(stream, x)))
@@ -616,7 +617,7 @@ def muon_fp8_grouped_wgrad(handle: int, yt, yt_scales, xt, xt_scales, offsets, d
     FP32."""
     (n, cap), k, e = yt.shape, xt.shape[0], offsets.shape[0] - 1
     _check(load_library().muon_fp8_grouped_wgrad(
-        handle, e, n, k, cap, _want("yt", yt, (n, cap), "e4m3"),
+        handle, e, n, k, cap, _want("yt", yt, None, "e4m3"),
         _want("yt_scales", yt_scales, (cap // 128, n), "e8m0"), _want("xt", xt, (k, cap), "e4m3"),
         _want("xt_scales", xt_scales, (cap // 128, k), "e8m0"),
         _want("offsets", offsets, (e + 1,), "i32"), _want("dw", dw, (e, n, k), "f32"),

@@ -197,3 +197,6 @@ def test_refusals(ns, h):
         ns.muon_moe_plan(h, ids, torch.zeros(17, dtype=torch.int32, device="cuda"), ids, torch.zeros_like(ids))
     with pytest.raises(ns.MuonError):            # too many experts
         ns.muon_moe_plan(h, ids, torch.zeros(1026, dtype=torch.int32, device="cuda"), torch.zeros_like(ids), torch.zeros_like(ids))
+    with pytest.raises(ValueError):              # y of another shape than its gradient
+        ns.muon_moe_combine_backward(h, torch.zeros(4, 32, dtype=torch.bfloat16, device="cuda"), y[:4], pos, None,
+                                     torch.zeros(8, 32, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 2, device="cuda"))
