@@ -484,7 +484,7 @@ muon_status_t muon_moe_route_backward(muon_handle_t handle, int64_t tokens, int3
 /* Grouping of slots by expert (a stable counting sort).  ids: [n_slots],
  * -1 for none.  offsets: [experts + 1]; slots: [n_slots], the slot of each
  * row, -1 past offsets[experts]; pos: [n_slots], the row of each slot or
- * -1.  Uses the handle's workspace when there are more than 4096 slots:
+ * -1.  Uses the handle's workspace when there are more than 2048 slots:
  * calls on several streams that use it (also muon_step's) are ordered by
  * the caller.  Errors: INVALID_ARG, NOMEM, CUDA. */
 muon_status_t muon_moe_plan(muon_handle_t handle, int64_t n_slots, int32_t experts,

@@ -30,7 +30,7 @@ def plan(ns, h, ids, experts, stream=None):
     return o, s, p
 
 
-@pytest.mark.parametrize("n", [0, 1, 31, 1000, 4095, 4096, 4097, 8192, 50001, 300000])
+@pytest.mark.parametrize("n", [0, 1, 31, 1024, 1025, 2048, 2049, 4095, 4096, 4097, 8192, 50001, 131073, 300000])
 @pytest.mark.parametrize("experts", [1, 7, 512, 1024])
 def test_plan(ns, h, n, experts):
     rng = np.random.default_rng(n + experts)
