@@ -156,7 +156,7 @@ __device__ __forceinline__ bool decode(const Fp8Args& p, const int32_t* first, c
   const int m = start[lo + 1] - start[lo];
   o.expert = lo;
   o.n0 = static_cast<int>(tm) * kTileM;
-  o.width = ((m + tiles - 1) / tiles + kWidthUnit - 1) / kWidthUnit * kWidthUnit;
+  o.width = min(kMaxTokens, ((m + tiles - 1) / tiles + kWidthUnit - 1) / kWidthUnit * kWidthUnit);
   o.c0 = start[lo] + i * o.width;
   o.cols = min(o.width, m - i * o.width);
   o.kb0 = 0;
@@ -165,13 +165,16 @@ __device__ __forceinline__ bool decode(const Fp8Args& p, const int32_t* first, c
   return true;
 }
 
-// Fills first[] and start[] (all threads, a few experts each).
+// Fills first[] and start[] (all threads, a few experts each).  Whatever offsets
+// holds, first[] rises no further than the buffers reach (64-bit sums: falling
+// offsets can count rows many times) and start[] stays within x and y.
 template <bool GRAD>
 __device__ __forceinline__ void scan_experts(const Fp8Args& p, int32_t* first, int32_t* start,
-                                             int32_t* warp_total) {
+                                             int64_t* warp_total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kPer = kMoeMaxExperts / Layout<GRAD>::kThreads + 1;   // and the end of the last
-  int count[kPer], sum = 0;
+  int count[kPer];
+  int64_t sum = 0;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -181,10 +184,10 @@ __device__ __forceinline__ void scan_experts(const Fp8Args& p, int32_t* first, i
       const int a = p.offsets[e], b = p.offsets[e + 1];
       if (GRAD) {
         bad = bad || a < 0 || b < a;
-        start[e] = max(0, b - a);
-        count[i] = (max(0, b - a) + kBK - 1) / kBK;
+        const int rows = a < 0 || b < a ? 0 : b - a;
+        start[e] = rows;
+        count[i] = rows / kBK + (rows % kBK != 0 ? 1 : 0);
       } else {
-        // Rows outside x and y are never touched, whatever offsets holds.
         const int top = static_cast<int>(p.rows);
         const int ca = min(max(a, 0), top), cb = min(max(b, ca), top);
         bad = bad || ca != a || cb != b;
@@ -195,23 +198,23 @@ __device__ __forceinline__ void scan_experts(const Fp8Args& p, int32_t* first, i
     }
     sum += count[i];
   }
-  int incl = sum;
+  int64_t incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
   if (lane == 31) warp_total[warp] = incl;
   __syncthreads();
-  int at = incl - sum;
+  int64_t at = incl - sum;
   for (int i = 0; i < warp; ++i) at += warp_total[i];
-  const int limit = GRAD ? static_cast<int>(p.rows / kBK) : INT32_MAX;
+  const int64_t limit = GRAD ? p.rows / kBK : p.rows / kMaxTokens + p.experts;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int e = threadIdx.x * kPer + i;
     if (e <= p.experts) {
       bad = bad || at > limit;
-      first[e] = min(at, limit);
+      first[e] = static_cast<int32_t>(min(at, limit));
     }
     at += count[i];
   }
@@ -343,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
   uint64_t* drain = tmem_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int32_t* warp_total = reinterpret_cast<int32_t*>(tmem_holder + 2);
+  int64_t* warp_total = reinterpret_cast<int64_t*>(tmem_holder + 2);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;

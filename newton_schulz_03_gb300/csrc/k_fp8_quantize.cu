@@ -297,41 +297,51 @@ __global__ void __launch_bounds__(kTileThreads, 3) quantize_cols_kernel(
   __shared__ uint2 col_max[kTileThreads / 32][32];
   __shared__ __align__(16) uint32_t row_at[kTileThreads / 32][16];   // a warp's rows
   __shared__ int32_t first[kMoeMaxExperts + 1];   // first row block of each expert
-  __shared__ int32_t warp_total[kTileThreads / 32];
+  __shared__ int64_t warp_total[kTileThreads / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
   grid_dep_launch();
 
-  // Row blocks before each expert: an exclusive scan, 4 experts per thread.
-  int count[4], sum = 0;
+  // Row blocks before each expert: an exclusive scan, 5 experts per thread (the
+  // end of the last among them).  64-bit sums, cut off past the buffers' end:
+  // falling offsets can count rows many times.
+  constexpr int kPer = kMoeMaxExperts / kTileThreads + 1;
+  const int64_t room = cap / 128;
+  int count[kPer];
+  int64_t sum = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = threadIdx.x * 4 + i;
-    count[i] = e < experts ? (max(0, offsets[e + 1] - offsets[e]) + 127) / 128 : 0;
+  for (int i = 0; i < kPer; ++i) {
+    const int e = threadIdx.x * kPer + i;
+    count[i] = 0;
+    if (e < experts) {
+      const int a = offsets[e], b = offsets[e + 1];
+      const int n = a < 0 || b < a ? 0 : b - a;
+      count[i] = n / 128 + (n % 128 != 0 ? 1 : 0);
+      if (n == 0 && a != b) atomicOr(err, kDevErrIndex);
+    }
     sum += count[i];
   }
-  int incl = sum;
+  int64_t incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(kAll, incl, o);
+    const int64_t v = __shfl_up_sync(kAll, incl, o);
     if (lane >= o) incl += v;
   }
   if (lane == 31) warp_total[warp] = incl;
   __syncthreads();
-  int at = incl - sum;
+  int64_t at = incl - sum;
   for (int i = 0; i < warp; ++i) at += warp_total[i];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = threadIdx.x * 4 + i;
-    if (e <= experts) first[e] = at;
+  for (int i = 0; i < kPer; ++i) {
+    const int e = threadIdx.x * kPer + i;
+    if (e <= experts) first[e] = static_cast<int32_t>(min(at, room + 1));
     at += count[i];
   }
-  if (threadIdx.x == kTileThreads - 1 && experts == 4 * kTileThreads) first[experts] = at;
   __syncthreads();
   int blocks = first[experts];
-  if (blocks > cap / 128) {                       // the caller's buffers are too short
+  if (blocks > room) {                            // the caller's buffers are too short
     if (threadIdx.x == 0) atomicOr(err, kDevErrIndex);
-    blocks = static_cast<int>(cap / 128);
+    blocks = static_cast<int>(room);
   }
   const int stripes = (d + 127) / 128;
   const int64_t units = static_cast<int64_t>((stripes + kStripes - 1) / kStripes) * blocks;

@@ -158,6 +158,30 @@ def test_bad_offsets_are_reported(ns, h):
         assert (whole[50:] == 9.0).all()
 
 
+def wild_offsets(experts, top):
+    """Offsets that no plan makes: falling, negative, past every buffer, rows counted many times."""
+    i = torch.arange(experts + 1)
+    big = 2**31 - 1
+    return [torch.where(i % 2 == 0, 0, top), torch.where(i % 2 == 0, 0, big), torch.where(i % 2 == 0, -big, big),
+            torch.where(i % 2 == 0, top, 0), i * (big // (experts + 1)), torch.where(i % 3 == 0, big, i)]
+
+
+@pytest.mark.parametrize("experts", [8, 600, 1024])
+def test_wild_offsets_stay_inside(ns, h, experts):
+    """Whatever offsets holds: an error, and not a byte outside the rows."""
+    r, n, k = 700, 48, 144
+    g = torch.Generator("cuda").manual_seed(1)
+    x, xs = fp8((r, k), g), scales((r, 2), g)
+    w, ws = fp8((experts, n, k), g), scales((experts, 1, 2), g)
+    whole = torch.full((r + 64, n), 9.0, dtype=torch.bfloat16, device="cuda")
+    for off in wild_offsets(experts, r):
+        ns.muon_fp8_grouped_matmul(h, x, xs, w, ws, off.int().cuda(), whole[32:r + 32])
+        with pytest.raises(ns.MuonError) as ei:
+            ns.muon_last_device_error(h)
+        assert ei.value.status_name == "MUON_ERR_INVALID_ARG"
+        assert (whole[:32] == 9.0).all() and (whole[r + 32:] == 9.0).all()
+
+
 # ------------------------------------------------------------------ weight gradient
 def wgrad_case(ns, counts, n, k, seed, extra=0):
     g = torch.Generator("cuda").manual_seed(seed)
@@ -221,6 +245,20 @@ def test_wgrad_capacity_too_small_is_reported(ns, h):
     with pytest.raises(ns.MuonError) as ei:
         ns.muon_last_device_error(h)
     assert ei.value.status_name == "MUON_ERR_INVALID_ARG"
+
+
+@pytest.mark.parametrize("experts", [8, 600, 1024])
+def test_wgrad_wild_offsets_stay_inside(ns, h, experts):
+    n, k, cap = 64, 80, 1024
+    g = torch.Generator("cuda").manual_seed(1)
+    ops = [fp8((n, cap), g), scales((cap // 128, n), g), fp8((k, cap), g), scales((cap // 128, k), g)]
+    whole = torch.full((experts + 2, n, k), 9.0, device="cuda")
+    for off in wild_offsets(experts, 700):
+        ns.muon_fp8_grouped_wgrad(h, *ops, off.int().cuda(), whole[1:experts + 1])
+        with pytest.raises(ns.MuonError) as ei:
+            ns.muon_last_device_error(h)
+        assert ei.value.status_name == "MUON_ERR_INVALID_ARG"
+        assert (whole[0] == 9.0).all() and (whole[-1] == 9.0).all()
 
 
 def test_quantised_gradient_against_differences(ns, h):

@@ -181,6 +181,25 @@ def test_too_short_a_buffer_is_reported(ns, h):
     assert (s[:, 0] == 127 - 8).all()
 
 
+@pytest.mark.parametrize("experts", [8, 600, 1024])
+def test_wild_offsets_stay_inside(ns, h, experts):
+    """Whatever offsets and slots hold: an error, and not a byte outside the buffers."""
+    i = torch.arange(experts + 1)
+    big = 2**31 - 1
+    x = torch.randn(50, 144, device="cuda").bfloat16()
+    slots = torch.randint(-5, 200, (150,), dtype=torch.int32, device="cuda")
+    qt = torch.full((146, 1024), 0x11, dtype=torch.uint8, device="cuda")
+    s = torch.full((10, 144), 0x22, dtype=torch.uint8, device="cuda")
+    for off in (torch.where(i % 2 == 0, 0, 150), torch.where(i % 2 == 0, 0, big), torch.where(i % 2 == 0, -big, big),
+                torch.where(i % 2 == 0, 150, 0), i * (big // (experts + 1)), torch.where(i % 3 == 0, big, i)):
+        for sl in (None, slots):
+            ns.muon_fp8_quantize_cols(h, x, off.int().cuda(), qt[1:145], s[1:9], slots=sl, top_k=3)
+            with pytest.raises(ns.MuonError) as ei:
+                ns.muon_last_device_error(h)
+            assert ei.value.status_name == "MUON_ERR_INVALID_ARG"
+            assert (qt[0] == 0x11).all() and (qt[145] == 0x11).all() and (s[0] == 0x22).all() and (s[9] == 0x22).all()
+
+
 @pytest.mark.parametrize("bad,byte", [(float("nan"), 0x7F), (float("inf"), 0x7E)])
 def test_nonfinite_values(ns, h, bad, byte):
     """NaN stays NaN, an infinity saturates; both are reported."""
