@@ -28,6 +28,13 @@
 // the next tile through the second accumulator, and the scales'.  The experts' rows
 // are read from `offsets` on the device: every block sums the experts' tile
 // counts before its first tile, so a call needs no host copy of the routing.
+//
+// Bound and measured (GB300).  Rows with few tokens per expert: reading w, 512
+// experts of 1536 x 4096 with 57344 rows 531-547 us (3.63 GB, 6.6-6.8 TB/s).
+// Dense: the tensor pipe at the power cap, 16381 x 6144 x 4096 240-280 us
+// (2.9-3.4 PFLOP/s, pipe 88% active).  One token through 7 experts: latency,
+// 14-15 us.  Weight gradient with few tokens per expert: writing dw, 64 experts
+// of 2048 x 8704 725-765 us (4.66 GB, 6.1-6.4 TB/s).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

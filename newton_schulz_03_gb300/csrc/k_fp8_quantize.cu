@@ -16,8 +16,11 @@
 //           operands of the weight gradient, whose sums run over rows (an
 //           expert's last block only as far as the next multiple of 32 rows)
 // A NaN stays NaN, an infinity becomes the largest value; both are reported
-// through the device error word.  Every kernel is bound by HBM: each value is
-// read once and written as one byte.
+// through the device error word.  Each value is read once and written as one
+// byte (two with the transpose): rows and blocks are bound by HBM (8192 tokens x
+// 4096 to 7 rows each 46.5 us, 6.5 TB/s; 48 FP32 weights of 2048 x 8704 in both
+// orientations 756 us, 6.8 TB/s), cols by its instructions (8191 x 4096 gathered
+// into 512 experts 109 us, 2.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
