@@ -217,6 +217,62 @@ def test_nonfinite_values(ns, h, bad, byte):
         assert int(s[0, 0]) == 127 - 8
 
 
+def finite_reference(x):
+    """Each value with NaN as zero and infinities as the largest BF16: what sets the scales."""
+    return np.nan_to_num(x, nan=0.0, posinf=3.3895314e38, neginf=-3.3895314e38)
+
+
+def test_nonfinite_columns(ns, h):
+    """One NaN, one infinity: their own columns' bytes, every scale and all other bytes as ever."""
+    off = np.array([0, 40, 40, 200], dtype=np.int32)
+    x = values(200, 272, 5)
+    x[3, 7] = float("nan")
+    x[199, 8] = float("inf")
+    x[60, 271] = float("-inf")
+    x[61, 271] = float("nan")
+    cap = ns.muon_fp8_cols_capacity(200, 3)
+    qt = torch.zeros(272, cap, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(cap // 128, 272, dtype=torch.uint8, device="cuda")
+    ns.muon_fp8_quantize_cols(h, x, torch.from_numpy(off).cuda(), qt, s)
+    with pytest.raises(ns.MuonError) as ei:
+        ns.muon_last_device_error(h)
+    assert ei.value.status_name == "MUON_ERR_NONFINITE"
+    want, ws = ref.quantize_cols(finite_reference(host(x)), off)
+    used, written = want.shape[1], ref.written_columns(off)
+    np.testing.assert_array_equal(s.cpu().numpy()[:used // 128], ws)
+    got, bytes_ = q_of(qt.view(F8))[:, :used], qt.cpu().numpy()
+    ok = np.tile(written, (272, 1))
+    starts = ref.padded_starts(off)
+    for row, col, byte in ((3, 7, 0x7F), (199, 8, 0x7E), (60, 271, 0xFE), (61, 271, 0x7F)):
+        e = 0 if row < 40 else 2
+        at = starts[e] + row - off[e]
+        assert bytes_[col, at] & (0x7F if byte == 0x7F else 0xFF) == byte
+        ok[col, at] = False
+    np.testing.assert_array_equal(got[ok], want[ok])
+
+
+def test_nonfinite_weights(ns, h):
+    w = torch.randn(2, 144, 272, device="cuda")
+    w[1, 130, 3] = float("nan")
+    w[0, 5, 200] = float("-inf")
+    q = torch.empty(2, 144, 272, dtype=torch.uint8, device="cuda")
+    s = torch.empty(2, 2, 3, dtype=torch.uint8, device="cuda")
+    qt = torch.empty(2, 272, 144, dtype=torch.uint8, device="cuda")
+    st = torch.empty(2, 3, 2, dtype=torch.uint8, device="cuda")
+    ns.muon_fp8_quantize_blocks(h, w, q, s, qt, st)
+    with pytest.raises(ns.MuonError) as ei:
+        ns.muon_last_device_error(h)
+    assert ei.value.status_name == "MUON_ERR_NONFINITE"
+    want, ws = ref.quantize_blocks(np.nan_to_num(w.double().cpu().numpy(), nan=0.0, neginf=-3.4028234e38))
+    np.testing.assert_array_equal(s.cpu().numpy(), ws)
+    assert int(q[1, 130, 3]) & 0x7F == 0x7F and int(q[0, 5, 200]) == 0xFE
+    assert torch.equal(qt, q.transpose(1, 2)) and torch.equal(st, s.transpose(1, 2))
+    got = q_of(q.view(F8))
+    ok = np.ones_like(want, dtype=bool)
+    ok[1, 130, 3] = ok[0, 5, 200] = False
+    np.testing.assert_array_equal(got[ok], want[ok])
+
+
 def test_subnormal_values(ns, h):
     w = torch.zeros(1, 128, 128, device="cuda")
     w[0, 3, 4] = 2.0 ** -140

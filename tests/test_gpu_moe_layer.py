@@ -156,3 +156,35 @@ def test_launches_are_counted(example):
         want = dict(moe_route=2, moe_plan=1, moe_combine=3, fp8_quantize=8, fp8_product=4, fp8_wgrad=2)
         assert {k: st["launches"][k] for k in want} == want
         assert all(st["total_ms"][k] > 0 for k in want)
+
+
+SCRIPT = """
+import hashlib, importlib.util, sys, torch
+spec = importlib.util.spec_from_file_location("m", "examples/moe_training_step.py")
+m = importlib.util.module_from_spec(spec); spec.loader.exec_module(m)
+with m.ns.Handle() as h:
+    layer = m.ExpertLayer(h.value, hidden=272, intermediate=144, experts=8, top_k=3, seed=3)
+    g = torch.Generator("cuda").manual_seed(5)
+    x = torch.randn(900, 272, generator=g, device="cuda").bfloat16()
+    y, saved = layer.forward(x)
+    gx = layer.backward(y, saved)
+    layer.step()
+    m.ns.muon_last_device_error(h.value)
+    d = hashlib.sha256()
+    for t in [y, gx] + layer.grads + layer.weights:
+        d.update(t.float().cpu().numpy().tobytes())
+print("digest", d.hexdigest())
+"""
+
+
+def test_same_with_and_without_launch_chaining(example):
+    """MUON_PDL=0 launches every kernel plainly: the same bits."""
+    import subprocess
+    import sys
+    out = []
+    for pdl in ("1", "0"):
+        r = subprocess.run([sys.executable, "-c", SCRIPT], cwd=ROOT, env=dict(os.environ, MUON_PDL=pdl), capture_output=True,
+                           text=True, timeout=600)
+        assert r.returncode == 0, r.stderr
+        out.append(r.stdout.split("digest ")[1].strip())
+    assert out[0] == out[1]

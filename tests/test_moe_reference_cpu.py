@@ -79,3 +79,17 @@ def test_column_capacity_holds_any_routing(rows, experts):
             left -= 1
     counts[0] += left
     assert (-(-counts // 128)).sum() * 128 <= cap
+
+
+def test_null_handle_is_refused():
+    """Every entry point of the layer checks its handle before anything else."""
+    import newton_schulz_03_gb300 as ns
+    from newton_schulz_03_gb300 import _native
+    lib = ns.load_library()
+    names = [n for n in ns.EXPORTED if n.startswith(("muon_moe_", "muon_fp8_"))]
+    assert len(names) == 10
+    for name in names:
+        fn = getattr(lib, name)
+        args = [None if t in (_native.ctypes.c_void_p,) or hasattr(t, "contents") else 0 for t in fn.argtypes]
+        assert fn(*args) == 1, name                  # MUON_ERR_INVALID_ARG
+        assert "handle" in ns.muon_last_error_message()
