@@ -69,8 +69,8 @@ struct Layout {
   // shared by kEpiWarps / 4 of them.  Rows: tiles with few K blocks are bound by
   // the epilogue.  Weight gradient: four with more staging each are faster.
   static constexpr int kEpiWarps = 4;
-  static constexpr int kScaleWarps = GRAD ? 2 : 4;
-  static constexpr int kSets = GRAD ? 4 : 8;                  // sets of scales in the ring
+  static constexpr int kScaleWarps = 4;                       // at most
+  static constexpr int kSets = 8;                             // sets of scales in the ring
   static constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
   static constexpr int kAccCols = GRAD ? kGradN : kMaxTokens;
   static constexpr int kStages = GRAD ? 5 : 6;                // operand stages, at most
@@ -100,6 +100,7 @@ struct Fp8Args {
   int32_t tiles_m, tiles_n;
   __nv_bfloat16* y;
   int32_t stages;       // operand stages in use
+  int32_t scale_warps;  // scale warps in use (a divisor of kSets)
   int32_t accumulate;
   int* err;
 };
@@ -338,7 +339,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
   using L = Layout<GRAD>;
   constexpr int kStages = L::kStages, kSets = L::kSets;
   const int stages = p.stages;
-  constexpr int kEpiWarps = L::kEpiWarps, kScaleWarps = L::kScaleWarps;
+  constexpr int kEpiWarps = L::kEpiWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -642,7 +643,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
     __syncwarp();
   } else {
     // ------------------------------------------------------------ scales (both CTAs)
-    // Warp `which` fills the sets which, which + kScaleWarps, ...; a set's loads
+    // Warp `which` fills the sets which, which + scale_warps, ...; a set's loads
     // are in flight while it waits for its place.  They follow the arrival for
     // the set before: a release waits for its thread's loads too.  A set takes a
     // warp some 3000 cycles (loads, proxy fence, release): four warps keep up
@@ -652,13 +653,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
     at.begin<GRAD>(p, first, start, pair);
     at.settle<GRAD>(p, first, start, npairs);
     at.advance<GRAD>(p, first, start, npairs, which);
+    if (which >= p.scale_warps) at.live = false;  // not in use
     int set = which;
     uint32_t set_phase = 0;
     bool ok = true;
     while (at.live) {
       uint32_t cells[kCells];
       load_set<GRAD>(p, at, rank, lane, cells);
-      at.advance<GRAD>(p, first, start, npairs, kScaleWarps);
+      at.advance<GRAD>(p, first, start, npairs, p.scale_warps);
       const bool got = ptx::mbar_wait_cluster(&set_empty[set], set_phase ^ 1u, abort_flag);
       if (!__all_sync(0xffffffffu, got)) {
         ok = false;
@@ -677,7 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
         else
           ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&set_full[set]), 0));
       }
-      set += kScaleWarps;
+      set += p.scale_warps;
       if (set >= kSets) {
         set -= kSets;
         set_phase ^= 1u;
@@ -795,6 +797,7 @@ cudaError_t launch_fp8_grouped_matmul(const uint8_t* x, const uint8_t* x_scales,
   p.k_blocks = (k + kBK - 1) / kBK;
   p.tiles_m = (n + kTileM - 1) / kTileM;
   p.stages = Layout<false>::kStages;
+  p.scale_warps = Layout<false>::kScaleWarps;
   p.y = reinterpret_cast<__nv_bfloat16*>(y);
   p.err = err;
   const int64_t token_tiles = (rows < experts ? rows : experts) + rows / kMaxTokens;
@@ -824,10 +827,12 @@ cudaError_t launch_fp8_grouped_wgrad(const uint8_t* yt, const uint8_t* yt_scales
   p.tiles_n = (k + kGradN - 1) / kGradN;
   // Few K blocks per expert: writing dw bounds the call, and pairs that load no
   // further than the next tile stay together, so that neighbouring tiles' rows
-  // leave L2 as whole runs.  Measured with 2 / 5 stages: 2.1 blocks per expert
-  // (2048 x 8704 x 16) 184 / 200 us, 2.7 (1536 x 4096 x 128) 587 / 680 us; 5.0
-  // (1536 x 4096 x 64) 437 / 305 us, 32 (2048 x 8704 x 8) 725 / 426 us.
-  p.stages = 2 * (cap / kBK) < 7 * static_cast<int64_t>(experts) ? 2 : Layout<true>::kStages;
+  // leave L2 as whole runs.  Measured with 2 stages and scale warps / 5 and 4:
+  // 2.0 blocks per expert (2048 x 8704 x 64) 726 / 832 us; 3.5 (1536 x 4096 x 64)
+  // 379 / 315 us; 32 (2048 x 8704 x 8) 727 / 403 us (2.9 PFLOP/s).
+  const bool few = 2 * (cap / kBK) < 5 * static_cast<int64_t>(experts);
+  p.stages = few ? 2 : Layout<true>::kStages;
+  p.scale_warps = few ? 2 : Layout<true>::kScaleWarps;
   p.accumulate = accumulate ? 1 : 0;
   p.err = err;
   return launch<true>(maps, p, int64_t(experts) * p.tiles_m * p.tiles_n, num_sms, s);
