@@ -226,6 +226,12 @@ __device__ __forceinline__ void scan_experts(const Fp8Args& p, int32_t* first, i
   if (bad && blockIdx.x == 0) atomicOr(p.err, kDevErrIndex);
 }
 
+// A wait by a whole warp with one outcome: when the limit expires in some lanes
+// only, all of them give up together (the warp stays converged for what follows).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+  return __all_sync(0xffffffffu, ptx::mbar_wait_cluster(bar, parity, abort));
+}
+
 // Walks the sets of scales of a pair's tiles.
 struct SetCursor {
   uint32_t t;
@@ -460,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
       Tile o;
       for (uint32_t t = pair; ok && decode<GRAD>(p, first, start, t, o); t += npairs) {
         if (o.nkb == 0) continue;
-        if (!ptx::mbar_wait_cluster(&tmem_empty[acc], acc_phase ^ 1u, abort_flag)) {
+        if (!warp_wait(&tmem_empty[acc], acc_phase ^ 1u, abort_flag)) {
           ok = false;
           break;
         }
@@ -469,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
         const uint32_t idesc0 = ptx::idesc_mxf8(kTileM, o.width);
         const bool wide = o.width > 128;
         for (int kb0 = 0; ok && kb0 < o.nkb; kb0 += kSetBlocks) {
-          if (!ptx::mbar_wait_cluster(&set_full[set], set_phase, abort_flag)) {
+          if (!warp_wait(&set_full[set], set_phase, abort_flag)) {
             ok = false;
             break;
           }
@@ -486,7 +492,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
 #pragma unroll
           for (int b = 0; b < kSetBlocks; ++b) {
             if (kb0 + b >= o.nkb) break;
-            if (!ptx::mbar_wait_cluster(&full[stage], phase, abort_flag)) {
+            if (!warp_wait(&full[stage], phase, abort_flag)) {
               ok = false;
               break;
             }
@@ -549,8 +555,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
       const bool empty_sum = o.nkb == 0;
       if (empty_sum && p.accumulate) continue;
       if (!empty_sum) {
-        const bool got = ptx::mbar_wait_cluster(&tmem_full[acc], acc_phase, abort_flag);
-        if (!__all_sync(0xffffffffu, got)) {
+        if (!warp_wait(&tmem_full[acc], acc_phase, abort_flag)) {
           if (lane == 0) {
             *abort_flag = 1;
             atomicOr(p.err, kDevErrTimeout);
@@ -658,8 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<GRAD>::kThrea
       uint32_t cells[kCells];
       load_set<GRAD>(p, at, rank, lane, cells);
       at.advance<GRAD>(p, first, start, npairs, p.scale_warps);
-      const bool got = ptx::mbar_wait_cluster(&set_empty[set], set_phase ^ 1u, abort_flag);
-      if (!__all_sync(0xffffffffu, got)) {
+      if (!warp_wait(&set_empty[set], set_phase ^ 1u, abort_flag)) {
         ok = false;
         break;
       }
