@@ -484,9 +484,11 @@ muon_status_t muon_moe_route_backward(muon_handle_t handle, int64_t tokens, int3
 /* Grouping of slots by expert (a stable counting sort).  ids: [n_slots],
  * -1 for none.  offsets: [experts + 1]; slots: [n_slots], the slot of each
  * row, -1 past offsets[experts]; pos: [n_slots], the row of each slot or
- * -1.  Uses the handle's workspace when there are more than 2048 slots:
- * calls on several streams that use it (also muon_step's) are ordered by
- * the caller.  Errors: INVALID_ARG, NOMEM, CUDA. */
+ * -1.  More than 2048 slots take scratch of the handle's, allocated at the
+ * first such call (512 KiB: enough for 2^20 slots) and again where a call
+ * needs more; none of it is freed before the handle, so a captured call stays
+ * valid whatever the handle does later.  Calls on several streams that use it
+ * are ordered by the caller.  Errors: INVALID_ARG, NOMEM, CUDA. */
 muon_status_t muon_moe_plan(muon_handle_t handle, int64_t n_slots, int32_t experts,
                             const int32_t* ids, int32_t* offsets, int32_t* slots, int32_t* pos,
                             void* stream);

@@ -18,9 +18,10 @@ struct HandleInfo {
 // makes the handle's device current.
 int handle_info(muon_handle_s* h, HandleInfo* out);
 
-// The handle's workspace, grown to at least `bytes` (a growth synchronises
-// the device).
-int handle_workspace(muon_handle_s* h, size_t bytes, void** out);
+// Device scratch of at least `bytes`, apart from the step's workspace.  Its
+// address outlives the call: a buffer that has become too small is kept until
+// the handle goes, since a captured graph may still write to it.
+int handle_scratch(muon_handle_s* h, size_t bytes, void** out);
 
 // Counts one kernel launch of class `kind` and, with timing on, brackets it
 // with events.

@@ -213,7 +213,7 @@ muon_status_t muon_moe_plan(muon_handle_t h, int64_t n_slots, int32_t experts, c
   void* scratch = nullptr;
   const size_t bytes = muon::moe_plan_scratch(n_slots, experts);
   if (bytes > 0)
-    MUON_TRY(static_cast<muon_status_t>(muon::handle_workspace(h, bytes, &scratch)));
+    MUON_TRY(static_cast<muon_status_t>(muon::handle_scratch(h, bytes, &scratch)));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (int phase = 2 - muon::moe_plan_launches(n_slots); phase < 2; ++phase) {
     muon::LaunchMark mark(h, MUON_KERNEL_MOE_PLAN, s);

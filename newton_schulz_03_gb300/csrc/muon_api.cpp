@@ -49,6 +49,7 @@ muon_status_t cuda_fail(cudaError_t e, const char* what) {
 
 constexpr size_t kDefaultWorkspace = size_t(8) << 30;  // 8 GiB
 constexpr size_t kAlign = 256;
+constexpr size_t kScratchBytes = size_t(512) << 10;    // any grouping of up to 2^20 slots
 using muon::kMaxDim;
 using muon::kMaxSteps;
 constexpr int64_t kMaxMatrixElems = int64_t(1) << 34;
@@ -201,6 +202,14 @@ struct muon_handle_s {
   void* ws = nullptr;
   size_t ws_size = 0;
   int* dev_err = nullptr;
+  // Scratch of the grouping: the last one is in use, none is freed before the
+  // handle (captured graphs hold their addresses).
+  struct Scratch {
+    void* ptr;
+    size_t bytes;
+  };
+  Scratch scratch[16] = {};                 // doubling from 512 KiB: 12 reach the longest grouping
+  int n_scratch = 0;
   // Host-buffer step: device staging ring, copy streams and their events.
   float* staging = nullptr;
   size_t staging_bytes = 0;
@@ -351,10 +360,25 @@ int handle_info(muon_handle_s* h, HandleInfo* out) {
   return MUON_OK;
 }
 
-int handle_workspace(muon_handle_s* h, size_t bytes, void** out) {
-  const muon_status_t st = ensure_workspace(h, bytes);
-  *out = h->ws;
-  return st;
+int handle_scratch(muon_handle_s* h, size_t bytes, void** out) {
+  const size_t last = h->n_scratch > 0 ? h->scratch[h->n_scratch - 1].bytes : 0;
+  if (last < bytes) {
+    // At least twice the last one: all of them are less than twice the last.
+    const size_t least = last == 0 ? kScratchBytes : 2 * last;
+    const size_t want = std::max(least, align_up(bytes, kAlign));
+    constexpr int kMost = sizeof(h->scratch) / sizeof(h->scratch[0]);
+    if (h->n_scratch == kMost) return fail(MUON_ERR_NOMEM, "the handle's scratch has grown %d times", kMost);
+    void* p = nullptr;
+    const cudaError_t e = cudaMalloc(&p, want);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return fail(MUON_ERR_NOMEM, "scratch allocation of %zu bytes failed: %s", want,
+                  cudaGetErrorString(e));
+    }
+    h->scratch[h->n_scratch++] = {p, want};
+  }
+  *out = h->scratch[h->n_scratch - 1].ptr;
+  return MUON_OK;
 }
 
 LaunchMark::LaunchMark(muon_handle_s* h, int kind, cudaStream_t s)
@@ -450,6 +474,7 @@ muon_status_t muon_destroy(muon_handle_t h) {
   }
   for (cudaEvent_t e : h->free_events) cudaEventDestroy(e);
   if (h->ws) cudaFree(h->ws);
+  for (int i = 0; i < h->n_scratch; ++i) cudaFree(h->scratch[i].ptr);
   if (h->staging) cudaFree(h->staging);
   if (h->copy_in) cudaStreamDestroy(h->copy_in);
   if (h->copy_out) cudaStreamDestroy(h->copy_out);
