@@ -129,7 +129,9 @@ const char* muon_version(void);
 /* Create a handle on `device` (-1 = the calling thread's current device).
  * `workspace_bytes_max` caps the device workspace the handle may allocate
  * (0 = default of 8 GiB); groups whose whole batch does not fit are
- * processed in chunks.  No device memory is allocated until first use.
+ * processed in chunks (a single matrix always gets room).  The scratch of
+ * muon_moe_plan is apart from it, and all of it together within the same
+ * cap: a grouping that needs more is refused (NOMEM).  No device memory is allocated until first use.
  * Errors: INVALID_ARG (out == NULL), NO_DEVICE, UNSUPPORTED_ARCH (not
  * sm_103), CUDA. */
 muon_status_t muon_create(muon_handle_t* out, int32_t device, size_t workspace_bytes_max);

@@ -363,9 +363,16 @@ int handle_info(muon_handle_s* h, HandleInfo* out) {
 int handle_scratch(muon_handle_s* h, size_t bytes, void** out) {
   const size_t last = h->n_scratch > 0 ? h->scratch[h->n_scratch - 1].bytes : 0;
   if (last < bytes) {
-    // At least twice the last one: all of them are less than twice the last.
+    // At least twice the last one (all of them are then less than twice the
+    // last) as far as the cap allows, which counts all of them.
+    size_t held = 0;
+    for (int i = 0; i < h->n_scratch; ++i) held += h->scratch[i].bytes;
+    const size_t room = h->ws_cap > held ? h->ws_cap - held : 0;
+    if (bytes > room)
+      return fail(MUON_ERR_NOMEM, "%zu bytes of scratch exceed the cap of %zu (%zu held)", bytes,
+                  h->ws_cap, held);
     const size_t least = last == 0 ? kScratchBytes : 2 * last;
-    const size_t want = std::max(least, align_up(bytes, kAlign));
+    const size_t want = std::min(std::max(least, align_up(bytes, kAlign)), room);
     constexpr int kMost = sizeof(h->scratch) / sizeof(h->scratch[0]);
     if (h->n_scratch == kMost) return fail(MUON_ERR_NOMEM, "the handle's scratch has grown %d times", kMost);
     void* p = nullptr;

@@ -87,3 +87,33 @@ def test_the_example_steps_between_capture_and_replay(ns):
         # roundings to BF16, and a choice on the edge in few tokens.
         assert float((a - b).norm() / b.norm()) <= 2.0**-7
         ns.muon_last_device_error(h.value)
+
+
+def test_scratch_keeps_to_the_cap(ns):
+    """workspace_bytes_max bounds what groupings take, all buffers together."""
+    experts = 1024
+
+    def call(h, n):
+        ids, out = random_ids(n, experts, n).cuda(), buffers(n, experts)
+        ns.muon_moe_plan(h.value, ids, *out)
+        for got, want in zip(out, ref.plan(ids.cpu().numpy(), experts)):
+            np.testing.assert_array_equal(got.cpu().numpy(), want)
+
+    # A chunk of 1024 slots takes a 4 KiB histogram here (up to 128 of them).
+    with ns.Handle(workspace_bytes_max=40960) as h:
+        call(h, 2048)                                     # no scratch
+        call(h, 10 * 1024)                                # all of the cap
+        with pytest.raises(ns.MuonError) as ei:
+            call(h, 10 * 1024 + 1)
+        assert ei.value.status_name == "MUON_ERR_NOMEM"
+        call(h, 10 * 1024)                                # as before
+    with ns.Handle(workspace_bytes_max=40960 - 1) as h:
+        with pytest.raises(ns.MuonError) as ei:
+            call(h, 10 * 1024)
+        assert ei.value.status_name == "MUON_ERR_NOMEM"
+    with ns.Handle(workspace_bytes_max=3 << 20) as h:
+        call(h, 1 << 20)                                  # 512 KiB
+        call(h, (1 << 20) + 1)                            # 1 MiB beside it
+        with pytest.raises(ns.MuonError):
+            call(h, 4 << 20)                              # 2 MiB are more than what is left
+        call(h, 3 << 20)                                  # 1.5 MiB are not: all that is left
