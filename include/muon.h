@@ -98,6 +98,15 @@ typedef struct {
   int64_t total_launches;               /* all kernel launches of the handle */
 } muon_kernel_stats_t;
 
+/* The same with the first nine classes alone: what muon_kernel_stats of
+ * version 0.1.0 wrote, and what the symbol of that name still writes. */
+#define MUON_KERNEL_COUNT_V1 9
+typedef struct {
+  double total_ms[MUON_KERNEL_COUNT_V1];
+  int64_t launches[MUON_KERNEL_COUNT_V1];
+  int64_t total_launches;               /* of all classes */
+} muon_kernel_stats_v1_t;
+
 /* Plan summary of a group list (pure host computation, no GPU needed). */
 typedef struct {
   int32_t n_batches;          /* distinct wide shapes (Newton-Schulz batches) */
@@ -584,9 +593,14 @@ muon_status_t muon_selftest_bounded_wait(muon_handle_t handle, int32_t limit_ms,
 /* Per-kernel timing: when enabled, every launch is bracketed by CUDA
  * events on the launching stream.  muon_kernel_stats synchronises the
  * device, folds the recorded events into `out` and keeps accumulating;
- * muon_reset_kernel_stats clears the totals. */
+ * muon_reset_kernel_stats clears the totals.
+ * The symbol muon_kernel_stats keeps the layout it had with nine classes, so
+ * that programs built against that header run on; sources that include this
+ * one call muon_kernel_stats_v2, with every class, under the same name. */
 muon_status_t muon_set_kernel_timing(muon_handle_t handle, int32_t enable);
-muon_status_t muon_kernel_stats(muon_handle_t handle, muon_kernel_stats_t* out);
+muon_status_t muon_kernel_stats(muon_handle_t handle, muon_kernel_stats_v1_t* out);
+muon_status_t muon_kernel_stats_v2(muon_handle_t handle, muon_kernel_stats_t* out);
+#define muon_kernel_stats muon_kernel_stats_v2
 muon_status_t muon_reset_kernel_stats(muon_handle_t handle);
 
 #ifdef __cplusplus

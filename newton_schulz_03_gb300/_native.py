@@ -32,7 +32,7 @@ EXPORTED = (
     "muon_status_string", "muon_last_error_message", "muon_version", "muon_create",
     "muon_destroy", "muon_plan_describe", "muon_step", "muon_step_host", "muon_momentum_cast",
     "muon_newton_schulz_bf16", "muon_apply_update", "muon_last_device_error",
-    "muon_set_kernel_timing", "muon_kernel_stats", "muon_reset_kernel_stats",
+    "muon_set_kernel_timing", "muon_kernel_stats", "muon_kernel_stats_v2", "muon_reset_kernel_stats",
     "muon_newton_schulz_bf16_static", "muon_selftest_bounded_wait", "muon_step_ex",
     "muon_adamw_step", "muon_partition", "muon_host_alloc", "muon_host_free",
     "muon_shard_momentum_cast", "muon_norm_from_sumsq", "muon_transpose_bf16", "muon_shard_apply",
@@ -59,6 +59,11 @@ class _Group(ctypes.Structure):
 class _Stats(ctypes.Structure):
     _fields_ = [("total_ms", ctypes.c_double * N_KERNELS),
                 ("launches", ctypes.c_int64 * N_KERNELS),
+                ("total_launches", ctypes.c_int64)]
+
+
+class _StatsV1(ctypes.Structure):
+    _fields_ = [("total_ms", ctypes.c_double * 9), ("launches", ctypes.c_int64 * 9),
                 ("total_launches", ctypes.c_int64)]
 
 
@@ -158,7 +163,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "muon_fp8_grouped_wgrad": (c_int, [c_vp, c_i32, c_i32, c_i32, c_i64, c_vp, c_vp, c_vp,
                                            c_vp, c_vp, c_vp, c_i32, c_vp]),
         "muon_set_kernel_timing": (c_int, [c_vp, c_i32]),
-        "muon_kernel_stats": (c_int, [c_vp, P(_Stats)]),
+        "muon_kernel_stats": (c_int, [c_vp, P(_StatsV1)]),
+        "muon_kernel_stats_v2": (c_int, [c_vp, P(_Stats)]),
         "muon_reset_kernel_stats": (c_int, [c_vp]),
     }
     for name, (res, args) in sig.items():
@@ -636,7 +642,7 @@ def muon_set_kernel_timing(handle: int, enable: bool) -> None:
 
 def muon_kernel_stats(handle: int) -> dict:
     st = _Stats()
-    _check(load_library().muon_kernel_stats(handle, ctypes.byref(st)))
+    _check(load_library().muon_kernel_stats_v2(handle, ctypes.byref(st)))
     return {"total_ms": {k: st.total_ms[i] for i, k in enumerate(KERNEL_NAMES)},
             "launches": {k: st.launches[i] for i, k in enumerate(KERNEL_NAMES)},
             "total_launches": st.total_launches}

@@ -426,7 +426,7 @@ const char* muon_status_string(muon_status_t s) {
 
 const char* muon_last_error_message(void) { return g_last_error.c_str(); }
 
-const char* muon_version(void) { return "muon-gb300 0.1.0 (sm_103a)"; }
+const char* muon_version(void) { return "muon-gb300 0.2.0 (sm_103a)"; }
 
 muon_status_t muon_create(muon_handle_t* out, int32_t device, size_t workspace_bytes_max) {
   if (out == nullptr) return fail(MUON_ERR_INVALID_ARG, "out is NULL");
@@ -1205,7 +1205,7 @@ muon_status_t muon_set_kernel_timing(muon_handle_t h, int32_t enable) {
   return MUON_OK;
 }
 
-muon_status_t muon_kernel_stats(muon_handle_t h, muon_kernel_stats_t* out) {
+muon_status_t muon_kernel_stats_v2(muon_handle_t h, muon_kernel_stats_t* out) {
   muon_status_t st = check_handle(h);
   if (st != MUON_OK) return st;
   if (out == nullptr) return fail(MUON_ERR_INVALID_ARG, "out is NULL");
@@ -1224,9 +1224,25 @@ muon_status_t muon_kernel_stats(muon_handle_t h, muon_kernel_stats_t* out) {
   return MUON_OK;
 }
 
+#undef muon_kernel_stats
+muon_status_t muon_kernel_stats(muon_handle_t h, muon_kernel_stats_v1_t* out) {
+  muon_status_t st = check_handle(h);
+  if (st != MUON_OK) return st;
+  if (out == nullptr) return fail(MUON_ERR_INVALID_ARG, "out is NULL");
+  muon_kernel_stats_t all;
+  st = muon_kernel_stats_v2(h, &all);
+  if (st != MUON_OK) return st;
+  for (int i = 0; i < MUON_KERNEL_COUNT_V1; ++i) {
+    out->total_ms[i] = all.total_ms[i];
+    out->launches[i] = all.launches[i];
+  }
+  out->total_launches = all.total_launches;
+  return MUON_OK;
+}
+
 muon_status_t muon_reset_kernel_stats(muon_handle_t h) {
   muon_kernel_stats_t tmp;
-  muon_status_t st = muon_kernel_stats(h, &tmp);  // drains pending events
+  muon_status_t st = muon_kernel_stats_v2(h, &tmp);  // drains pending events
   if (st != MUON_OK) return st;
   h->stats = muon_kernel_stats_t{};
   return MUON_OK;
