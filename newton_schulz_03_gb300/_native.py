@@ -562,11 +562,16 @@ def muon_fp8_quantize_rows(handle: int, x, q, scales, pos=None, offsets=None,
         k = pos.shape[-1]
     elif r != t:
         raise ValueError(f"q must have {t} rows, got {r}")
+    live = 0
+    if offsets is not None:
+        if offsets.numel() == 0:
+            raise ValueError("offsets must not be empty")
+        live = _want("offsets", offsets, None, "i32") + 4 * (offsets.numel() - 1)
     _check(load_library().muon_fp8_quantize_rows(
         handle, t, d, _want("x", x, None, "bf16"),
         0 if pos is None else _want("pos", pos, (t, k), "i32"), k, r,
-        0 if offsets is None else _want("offsets", offsets, offsets.shape, "i32") + 4 * (offsets.numel() - 1),
-        _want("q", q, (r, d), "e4m3"), _want("scales", scales, (r, _nb(d)), "e8m0"), _stream_of(stream, x)))
+        live, _want("q", q, (r, d), "e4m3"), _want("scales", scales, (r, _nb(d)), "e8m0"),
+        _stream_of(stream, x)))
 
 
 def muon_fp8_quantize_blocks(handle: int, w, q=None, scales=None, qt=None, scales_t=None,

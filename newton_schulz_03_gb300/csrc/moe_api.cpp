@@ -40,16 +40,17 @@ struct Buffer {
   const void* ptr;
   int64_t bytes;
   bool out;
+  int align = 16;
 };
 
-// Every buffer present, 16-byte aligned, no output overlapping another.
+// Every buffer present and aligned, no output overlapping another.
 template <int N>
 muon_status_t check_buffers(const Buffer (&b)[N]) {
   for (int i = 0; i < N; ++i) {
     if (b[i].bytes == 0) continue;               // not wanted
     if (b[i].ptr == nullptr) return fail(MUON_ERR_INVALID_ARG, "NULL buffer");
-    if ((reinterpret_cast<uintptr_t>(b[i].ptr) & 15u) != 0)
-      return fail(MUON_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(b[i].ptr) % static_cast<uintptr_t>(b[i].align) != 0)
+      return fail(MUON_ERR_INVALID_ARG, "buffers must be %d-byte aligned", b[i].align);
   }
   for (int i = 0; i < N; ++i)
     for (int j = 0; j < i; ++j) {
@@ -287,8 +288,9 @@ muon_status_t muon_fp8_quantize_rows(muon_handle_t h, int64_t tokens, int32_t hi
   if (threads / 256 >= (int64_t(1) << 31) - 1)
     return fail(MUON_ERR_INVALID_ARG, "x is too large for one call");
   if (tokens == 0) return MUON_OK;
-  MUON_TRY(check_buffers<4>({{x, tokens * hidden * 2, false},
+  MUON_TRY(check_buffers<5>({{x, tokens * hidden * 2, false},
                              {pos, pos != nullptr ? tokens * top_k * 4 : 0, false},
+                             {live_rows, live_rows != nullptr ? 4 : 0, false, 4},
                              {q, rows * hidden, true},
                              {scales, rows * blocks_of(hidden), true}}));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
