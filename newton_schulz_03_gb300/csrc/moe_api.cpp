@@ -83,7 +83,7 @@ muon_status_t check_experts(int32_t experts) {
 muon_status_t check_slots(int64_t tokens, int32_t top_k) {
   if (top_k < 1 || top_k > muon::kMoeMaxTopK)
     return fail(MUON_ERR_INVALID_ARG, "top_k must be 1..%d (got %d)", muon::kMoeMaxTopK, top_k);
-  if (tokens < 0 || tokens * top_k > kMaxSlots)
+  if (tokens < 0 || tokens > kMaxSlots / top_k)       // the product may not fit 64 bits
     return fail(MUON_ERR_INVALID_ARG, "tokens out of range (%lld)", static_cast<long long>(tokens));
   return MUON_OK;
 }

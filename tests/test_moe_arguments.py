@@ -48,3 +48,23 @@ def test_live_rows_are_checked(ns, h):
     torch.cuda.synchronize()
     assert (q[:2] != 0).all() and (q[2:] == 0).all()
     ns.muon_last_device_error(h)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens,k", [(1 << 60, 16), (1 << 59, 32), (1 << 62, 4), ((1 << 63) - 1, 2), ((1 << 31) - (1 << 20) + 1, 1),
+                                      (-1, 1), (-(1 << 62), 4)])
+def test_token_counts_whose_slots_do_not_fit(ns, h, tokens, k):
+    """tokens x top_k past 2^31 is refused, past 2^64 too (the product would
+    come out as zero).  No buffer is behind the pointers: nothing is launched."""
+    lib, p = ns.load_library(), ctypes.c_void_p
+    a = [p(4096 * (i + 1)) for i in range(6)]
+    opts = (ctypes.c_int32 * 6)(0, 1, 1, 1, 1, 0x3F800000)
+    opts = ctypes.cast(opts, lib.muon_moe_route.argtypes[8])
+    before = ns.muon_kernel_stats(h)["total_launches"]
+    assert lib.muon_moe_route(h, tokens, 64, k, a[0], 0, p(0), p(0), opts, a[1], a[2], p(0)) == 1
+    assert lib.muon_moe_route_backward(h, tokens, 64, k, a[0], 0, a[1], a[2], opts, a[3], p(0)) == 1
+    assert lib.muon_moe_combine(h, tokens, k, 8, 32, a[0], a[1], p(0), a[2], p(0)) == 1
+    assert lib.muon_moe_combine_backward(h, tokens, k, 8, 32, a[0], p(0), a[1], p(0), a[2], p(0), p(0)) == 1
+    assert lib.muon_fp8_quantize_rows(h, tokens, 32, a[0], a[1], k, 8, p(0), a[2], a[3], p(0)) == 1
+    assert "tokens out of range" in ns.muon_last_error_message()
+    assert ns.muon_kernel_stats(h)["total_launches"] == before
