@@ -141,8 +141,9 @@ muon_status_t muon_moe_route(muon_handle_t h, int64_t tokens, int32_t experts, i
                 opts->top_groups);
   if (tokens == 0) return MUON_OK;
   const int64_t el = logits_type == MUON_BF16 ? 2 : 4;
-  MUON_TRY(check_buffers<4>({{logits, tokens * experts * el, false},
+  MUON_TRY(check_buffers<5>({{logits, tokens * experts * el, false},
                              {bias, bias != nullptr ? int64_t(experts) * 4 : 0, false},
+                             {mask, mask != nullptr ? tokens : 0, false, 1},
                              {ids, tokens * top_k * 4, true},
                              {weights, tokens * top_k * 4, true}}));
   muon::RouteArgs a{};

@@ -68,3 +68,22 @@ def test_token_counts_whose_slots_do_not_fit(ns, h, tokens, k):
     assert lib.muon_fp8_quantize_rows(h, tokens, 32, a[0], a[1], k, 8, p(0), a[2], a[3], p(0)) == 1
     assert "tokens out of range" in ns.muon_last_error_message()
     assert ns.muon_kernel_stats(h)["total_launches"] == before
+
+
+@pytest.mark.gpu
+def test_the_mask_is_not_an_output(ns, h):
+    """A mask under ids or weights would be overwritten while others read it."""
+    x = torch.randn(64, 32, device="cuda")
+    ids, w = torch.zeros(64, 2, dtype=torch.int32, device="cuda"), torch.zeros(64, 2, device="cuda")
+    for out in (ids, w):
+        for first in (0, 7, 448):
+            mask = out.view(torch.uint8).view(-1)[first:first + 64]
+            with pytest.raises(ns.MuonError) as ei:
+                ns.muon_moe_route(h, x, ids, w, mask=mask)
+            assert ei.value.status_name == "MUON_ERR_INVALID_ARG"
+    # A mask may start at any byte.
+    mask = torch.ones(67, dtype=torch.uint8, device="cuda")
+    mask[3] = 0
+    ns.muon_moe_route(h, x, ids, w, mask=mask[3:])
+    assert (ids[0] == -1).all() and (ids[1:] >= 0).all()
+    ns.muon_last_device_error(h)
