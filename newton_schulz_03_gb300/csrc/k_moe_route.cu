@@ -8,7 +8,7 @@
 // asked.  The bias chooses, it does not weigh.
 // Backward: with g the gradient of w and w the weights over `scale`,
 //   sigmoid          dx_j = scale g_j s_j (1 - s_j)
-//   sigmoid, renorm  dx_j = scale (g_j - sum_i g_i w_i) / S  s_j (1 - s_j)
+//   sigmoid, renorm  dx_j = scale w_j (g_j - sum_i g_i w_i) (1 - s_j)
 //   softmax          dx_e = s_e (scale g_e - sum_i scale g_i s_i), every open e
 //   softmax, renorm  dx_j = scale w_j (g_j - sum_i g_i w_i)
 // Scores are recomputed from the logits: they cost a few instructions, storing
@@ -602,16 +602,17 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const Route
     } else {
       // 1 - s as sigmoid(-x): no cancellation for large x.
       const float s = id >= 0 ? sigmoid(xj) : 0.f;
-      const float ds = id >= 0 ? s * sigmoid(-xj) : 0.f;
+      const float rest = id >= 0 ? sigmoid(-xj) : 0.f;
       if (a.renorm) {
         // Through the weights: a single choice's is exactly 1, and its
-        // gradient exactly 0.
+        // gradient exactly 0.  They are at most 1 where the scores' sum is
+        // next to nothing: no quotient by it, which could overflow.
         const float sum = warp_sum(s);
         const float share = sum > 0.f ? s / sum : 0.f;
         const float dot = warp_sum(id >= 0 ? g * share : 0.f);
-        dx = sum > 0.f ? (g - dot) / sum * ds : 0.f;
+        dx = share * (g - dot) * rest;
       } else {
-        dx = g * ds;
+        dx = g * (s * rest);
       }
     }
   }

@@ -237,3 +237,35 @@ def test_binding_refusals(ns, h):
             ns.muon_moe_route(h, kw.pop("logits"), kw.pop("ids"), kw.pop("weights"), **kw)
     with pytest.raises(ns.MuonError):
         ns.muon_moe_route(h, x.view(-1)[1:].clone().as_strided((1, 32), (32, 1), 1), ids[:1], w[:1])  # not 16-byte aligned
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("k", [2, 5])
+def test_small_scores_have_finite_gradients(ns, h, dtype, k):
+    """All chosen sigmoids between 1e-39 and 1e-30, gradients up to a loss
+    scale's: the renormalised weights are ordinary, and so is their gradient."""
+    t, e, scale = 400, 64, 2.5
+    g = torch.Generator("cuda").manual_seed(k)
+    x = (-70.0 - 18.5 * torch.rand(t, e, generator=g, device="cuda")).to(getattr(torch, dtype))
+    x[0], x[1] = -88.5, -80.0
+    ids, w = run(ns, h, x, k, scale=scale)
+    x64 = x.double().cpu().numpy()
+    # A score is off by 2 ulp of the exponential, half an ulp of the sum, of the
+    # reciprocal and of the subnormal result (2^-149 of 3.7e-39): 6e-7; a weight by
+    # two scores', the sum's and the division's: 1.5e-6.
+    share = ref.weights_of(x64, ids, softmax=False, renorm=True, scale=1.0)
+    np.testing.assert_allclose(w, scale * share, rtol=3e-6)
+    grad = torch.randn(t, k, generator=g, device="cuda")
+    grad[1::2] *= 2e4
+    out = torch.full((t, e), float("nan"), dtype=x.dtype, device="cuda")
+    ns.muon_moe_route_backward(h, x, torch.from_numpy(ids).cuda(), grad, out, scale=scale)
+    got, want = out.double().cpu().numpy(), ref.route_backward(x64, ids, grad.double().cpu().numpy(), softmax=False,
+                                                               renorm=True, scale=scale)
+    assert np.isfinite(got).all() and np.abs(want).max() > 1e3
+    # dx = w (g - <g, w>) (1 - s): the weight's 1.5e-6 of a difference of up to
+    # twice the largest gradient, and the sum's 2e-6 of it; BF16 adds half an ulp.
+    full = np.zeros_like(want)
+    np.put_along_axis(full, ids.astype(np.int64), share, 1)
+    tol = 8e-6 * scale * np.abs(grad.double().cpu().numpy()).max(1, keepdims=True) * full
+    assert (np.abs(got - want) <= tol + (np.abs(want) / 256 if dtype == "bfloat16" else 0.0)).all()
+    ns.muon_last_device_error(h)
