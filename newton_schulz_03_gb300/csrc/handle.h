@@ -5,12 +5,15 @@
 
 #include <cstddef>
 
+#include "moe.h"
+
 struct muon_handle_s;
 
 namespace muon {
 
 struct HandleInfo {
   int num_sms;
+  Fp8Pairs fp8_pairs;
   int* dev_err;   // device error word (kDevErr* bits)
 };
 

@@ -739,23 +739,22 @@ bool encode(CUtensorMap* map, bool fp32, const void* ptr, int64_t cols, int64_t 
 }
 
 template <bool GRAD>
-cudaError_t launch(const Maps& maps, const Fp8Args& p, int64_t max_tiles, int num_sms,
+cudaError_t setup(int num_sms, int* pairs) {
+  const cudaError_t e = cudaFuncSetAttribute(
+      fp8_product_kernel<GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<GRAD>::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(Layout<GRAD>::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Layout<GRAD>::kSmem;
+  return resident_pairs(
+      [&](int* n) { return cudaOccupancyMaxActiveClusters(n, fp8_product_kernel<GRAD>, &cfg); },
+      num_sms, pairs);
+}
+
+template <bool GRAD>
+cudaError_t launch(const Maps& maps, const Fp8Args& p, int64_t max_tiles, int64_t pairs,
                    cudaStream_t s) {
-  static int resident = 0;                        // pairs that fit the GPU at once
-  if (resident == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2, 1, 1);
-    cfg.blockDim = dim3(Layout<GRAD>::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = Layout<GRAD>::kSmem;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_product_kernel<GRAD>, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      n = 1;
-    }
-    resident = n;
-  }
-  int64_t pairs = resident;
-  if (pairs > num_sms / 2) pairs = num_sms / 2;
   if (pairs > max_tiles) pairs = max_tiles;
   if (pairs < 1) pairs = 1;
   if (max_tiles + 2 * pairs >= INT32_MAX) return cudaErrorInvalidValue;   // tile numbers are 32 bits
@@ -766,20 +765,15 @@ cudaError_t launch(const Maps& maps, const Fp8Args& p, int64_t max_tiles, int nu
 
 }  // namespace
 
-cudaError_t fp8_gemm_init() {
-  cudaError_t e = cudaFuncSetAttribute(fp8_product_kernel<false>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Layout<false>::kSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(fp8_product_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Layout<true>::kSmem);
-  return e;
+cudaError_t fp8_gemm_init(int num_sms, Fp8Pairs* pairs) {
+  const cudaError_t e = setup<false>(num_sms, &pairs->matmul);
+  return e != cudaSuccess ? e : setup<true>(num_sms, &pairs->wgrad);
 }
 
 cudaError_t launch_fp8_grouped_matmul(const uint8_t* x, const uint8_t* x_scales, const uint8_t* w,
                                       const uint8_t* w_scales, const int32_t* offsets, int experts,
-                                      int64_t rows, int n, int k, uint16_t* y, int* err,
-                                      int num_sms, cudaStream_t s) {
+                                      int64_t rows, int n, int k, uint16_t* y, int* err, int pairs,
+                                      cudaStream_t s) {
   Maps maps;
   bool ok = encode(&maps.a, false, w, k, n, experts, kBK, kHalfM);
   for (int i = 0; i < kMaps; ++i)
@@ -802,13 +796,13 @@ cudaError_t launch_fp8_grouped_matmul(const uint8_t* x, const uint8_t* x_scales,
   p.y = reinterpret_cast<__nv_bfloat16*>(y);
   p.err = err;
   const int64_t token_tiles = (rows < experts ? rows : experts) + rows / kMaxTokens;
-  return launch<false>(maps, p, token_tiles * p.tiles_m, num_sms, s);
+  return launch<false>(maps, p, token_tiles * p.tiles_m, pairs, s);
 }
 
 cudaError_t launch_fp8_grouped_wgrad(const uint8_t* yt, const uint8_t* yt_scales,
                                      const uint8_t* xt, const uint8_t* xt_scales,
                                      const int32_t* offsets, int experts, int64_t cap, int n, int k,
-                                     float* dw, bool accumulate, int* err, int num_sms,
+                                     float* dw, bool accumulate, int* err, int pairs,
                                      cudaStream_t s) {
   Maps maps;
   bool ok = encode(&maps.a, false, yt, cap, n, 1, kBK, kHalfM);
@@ -836,7 +830,7 @@ cudaError_t launch_fp8_grouped_wgrad(const uint8_t* yt, const uint8_t* yt_scales
   p.scale_warps = few ? 2 : Layout<true>::kScaleWarps;
   p.accumulate = accumulate ? 1 : 0;
   p.err = err;
-  return launch<true>(maps, p, int64_t(experts) * p.tiles_m * p.tiles_n, num_sms, s);
+  return launch<true>(maps, p, int64_t(experts) * p.tiles_m * p.tiles_n, pairs, s);
 }
 
 }  // namespace muon

@@ -55,9 +55,28 @@ cudaError_t launch_moe_combine_backward(const uint16_t* grad_out, const uint16_t
                                         int* err, cudaStream_t s);
 
 // ------------------------------------------------------------------ FP8
-// Shared-memory attributes of the kernels (called when a handle is made).
+// CTA pairs of the products' persistent grids on a handle's device.
+struct Fp8Pairs {
+  int matmul, wgrad;
+};
+
+// Pairs of such a grid: what `query` (an int* to how many clusters the GPU
+// holds at once) says, at most one pair per two SMs.  A query that fails, or
+// finds no room, is an error and leaves *out alone.
+template <typename Query>
+cudaError_t resident_pairs(Query query, int num_sms, int* out) {
+  int n = 0;
+  const cudaError_t e = query(&n);
+  if (e != cudaSuccess) return e;
+  if (n < 1 || num_sms < 2) return cudaErrorInvalidConfiguration;
+  *out = n < num_sms / 2 ? n : num_sms / 2;
+  return cudaSuccess;
+}
+
+// Shared-memory attributes of the kernels, and the products' pairs (called
+// when a handle is made, with its device current).
 cudaError_t moe_plan_init();
-cudaError_t fp8_gemm_init();
+cudaError_t fp8_gemm_init(int num_sms, Fp8Pairs* pairs);
 
 constexpr int kFp8Block = 128;   // values that share one scale
 
@@ -88,8 +107,8 @@ cudaError_t launch_fp8_quantize_cols(const uint16_t* x, int64_t x_rows, int d,
 // (nb, kb: blocks of 128), y BF16 [rows][n].
 cudaError_t launch_fp8_grouped_matmul(const uint8_t* x, const uint8_t* x_scales, const uint8_t* w,
                                       const uint8_t* w_scales, const int32_t* offsets, int experts,
-                                      int64_t rows, int n, int k, uint16_t* y, int* err,
-                                      int num_sms, cudaStream_t s);
+                                      int64_t rows, int n, int k, uint16_t* y, int* err, int pairs,
+                                      cudaStream_t s);
 
 // dw[e] (+)= the expert's columns of yt times those of xt transposed: yt
 // e4m3 [n][cap], scales [cap / 128][n]; xt [k][cap], [cap / 128][k]; dw FP32
@@ -97,7 +116,7 @@ cudaError_t launch_fp8_grouped_matmul(const uint8_t* x, const uint8_t* x_scales,
 cudaError_t launch_fp8_grouped_wgrad(const uint8_t* yt, const uint8_t* yt_scales,
                                      const uint8_t* xt, const uint8_t* xt_scales,
                                      const int32_t* offsets, int experts, int64_t cap, int n, int k,
-                                     float* dw, bool accumulate, int* err, int num_sms,
+                                     float* dw, bool accumulate, int* err, int pairs,
                                      cudaStream_t s);
 
 }  // namespace muon

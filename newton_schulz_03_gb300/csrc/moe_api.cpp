@@ -380,7 +380,7 @@ muon_status_t muon_fp8_grouped_matmul(muon_handle_t h, int64_t rows, int32_t exp
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   muon::LaunchMark mark(h, MUON_KERNEL_FP8_PRODUCT, s);
   return launched(muon::launch_fp8_grouped_matmul(x, x_scales, w, w_scales, offsets, experts, rows,
-                                                  n, k, y, hi.dev_err, hi.num_sms, s),
+                                                  n, k, y, hi.dev_err, hi.fp8_pairs.matmul, s),
                   "grouped product");
 }
 
@@ -407,7 +407,7 @@ muon_status_t muon_fp8_grouped_wgrad(muon_handle_t h, int32_t experts, int32_t n
   muon::LaunchMark mark(h, MUON_KERNEL_FP8_WGRAD, s);
   return launched(muon::launch_fp8_grouped_wgrad(yt, yt_scales, xt, xt_scales, offsets, experts,
                                                  capacity, n, k, dw, accumulate != 0, hi.dev_err,
-                                                 hi.num_sms, s),
+                                                 hi.fp8_pairs.wgrad, s),
                   "weight gradient");
 }
 

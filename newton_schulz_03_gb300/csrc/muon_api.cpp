@@ -198,6 +198,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 struct muon_handle_s {
   int device = 0;
   int num_sms = 0;
+  muon::Fp8Pairs fp8_pairs{};
   size_t ws_cap = kDefaultWorkspace;
   void* ws = nullptr;
   size_t ws_size = 0;
@@ -356,6 +357,7 @@ int handle_info(muon_handle_s* h, HandleInfo* out) {
   const muon_status_t st = check_handle(h);
   if (st != MUON_OK) return st;
   out->num_sms = h->num_sms;
+  out->fp8_pairs = h->fp8_pairs;
   out->dev_err = h->dev_err;
   return MUON_OK;
 }
@@ -454,11 +456,13 @@ muon_status_t muon_create(muon_handle_t* out, int32_t device, size_t workspace_b
   if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
   e = muon::ns_gemm_init();
   if (e == cudaSuccess) e = muon::moe_plan_init();
-  if (e == cudaSuccess) e = muon::fp8_gemm_init();
+  muon::Fp8Pairs pairs{};
+  if (e == cudaSuccess) e = muon::fp8_gemm_init(sms, &pairs);
   if (e != cudaSuccess) return cuda_fail(e, "kernel attribute setup");
   muon_handle_t h = new muon_handle_s();
   h->device = device;
   h->num_sms = sms;
+  h->fp8_pairs = pairs;
   h->ws_cap = workspace_bytes_max == 0 ? kDefaultWorkspace : workspace_bytes_max;
   e = cudaMalloc(reinterpret_cast<void**>(&h->dev_err), 256);
   if (e != cudaSuccess) {
