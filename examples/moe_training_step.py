@@ -77,7 +77,7 @@ class ExpertLayer:
 
     def _cols(self, x, offsets, rows, slots=None):
         """x in FP8 columns of each expert's rows, for a weight gradient."""
-        cap, d = max(128, ns.muon_fp8_cols_capacity(rows, self.experts)), x.shape[1]
+        cap, d = ns.muon_fp8_cols_capacity(rows, self.experts), x.shape[1]
         q = torch.empty(d, cap, dtype=F8, device=x.device)
         s = torch.empty(cap // 128, d, dtype=torch.uint8, device=x.device)
         ns.muon_fp8_quantize_cols(self.h, x, offsets, q, s, slots=slots, top_k=self.top_k)

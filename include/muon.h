@@ -551,7 +551,8 @@ muon_status_t muon_fp8_quantize_blocks(muon_handle_t handle, int32_t experts, in
  * to the next multiple of 32, and what is left of its last 128 is not written
  * (muon_fp8_grouped_wgrad does not use it), nor are columns past the last
  * expert's.  scales: [capacity / 128][hidden].  capacity is a multiple of
- * 128; rows + 127 experts, rounded down to one, always suffices.  Row r is
+ * 128; rows + 127 experts, rounded down to one, always suffices (0 for no
+ * rows: muon_fp8_grouped_wgrad takes that too).  Row r is
  * x[r] of x [x_rows][hidden] (BF16), or x[slots[r] / top_k] with slots [rows]
  * from muon_moe_plan. */
 muon_status_t muon_fp8_quantize_cols(muon_handle_t handle, int64_t x_rows, int32_t hidden,
@@ -575,7 +576,8 @@ muon_status_t muon_fp8_grouped_matmul(muon_handle_t handle, int64_t rows, int32_
  * expert, FP32 (with accumulate: added to dw).  yt [n][capacity] and xt
  * [k][capacity] with their scales as muon_fp8_quantize_cols gives them for
  * these offsets; dw [experts][n][k], the layout of muon_step's gradients.
- * An expert without rows gets zeros (or keeps what it has). */
+ * An expert without rows gets zeros (or keeps what it has); with a capacity
+ * of 0 that is all of them, and yt, xt and their scales may be NULL. */
 muon_status_t muon_fp8_grouped_wgrad(muon_handle_t handle, int32_t experts, int32_t n, int32_t k,
                                      int64_t capacity, const uint8_t* yt, const uint8_t* yt_scales,
                                      const uint8_t* xt, const uint8_t* xt_scales,

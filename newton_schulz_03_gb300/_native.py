@@ -591,7 +591,7 @@ def muon_fp8_quantize_blocks(handle: int, w, q=None, scales=None, qt=None, scale
 
 def muon_fp8_cols_capacity(rows: int, experts: int) -> int:
     """Columns that hold ``rows`` rows of ``experts`` experts, each expert's
-    rounded up to a multiple of 128, however they fall."""
+    rounded up to a multiple of 128, however they fall (0 for no rows)."""
     return (rows + 127 * min(experts, rows)) // 128 * 128
 
 

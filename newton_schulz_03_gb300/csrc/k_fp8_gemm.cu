@@ -805,9 +805,13 @@ cudaError_t launch_fp8_grouped_wgrad(const uint8_t* yt, const uint8_t* yt_scales
                                      float* dw, bool accumulate, int* err, int pairs,
                                      cudaStream_t s) {
   Maps maps;
-  bool ok = encode(&maps.a, false, yt, cap, n, 1, kBK, kHalfM);
-  ok = ok && encode(&maps.b[0], false, xt, cap, k, 1, kBK, kGradN / 2);
-  ok = ok && encode(&maps.out, true, dw, k, n, experts, 32, 32);
+  bool ok = encode(&maps.out, true, dw, k, n, experts, 32, 32);
+  if (cap > 0) {
+    ok = ok && encode(&maps.a, false, yt, cap, n, 1, kBK, kHalfM);
+    ok = ok && encode(&maps.b[0], false, xt, cap, k, 1, kBK, kGradN / 2);
+  } else {
+    maps.a = maps.b[0] = maps.out;                // no K block: nothing is loaded
+  }
   if (!ok) return cudaErrorInvalidValue;
   for (int i = 1; i < kMaps; ++i) maps.b[i] = maps.b[0];
   Fp8Args p{};

@@ -576,7 +576,8 @@ cudaError_t launch_fp8_quantize_cols(const uint16_t* x, int64_t x_rows, int d,
                                      int top_k, int64_t rows, uint8_t* qt, int64_t cap,
                                      uint8_t* scales, int* err, int num_sms, cudaStream_t s) {
   const int64_t tiles = (cap / 128) * ((d + 127) / 128);
-  const int64_t grid = tiles < 3 * num_sms ? tiles : 3 * num_sms;   // three blocks per SM
+  int64_t grid = tiles < 3 * num_sms ? tiles : 3 * num_sms;   // three blocks per SM
+  if (grid < 1) grid = 1;                          // no columns: rows in offsets are reported
   return launch_pdl(quantize_cols_kernel, dim3(static_cast<unsigned>(grid)), dim3(kTileThreads), 0, s,
                     x, x_rows, d, offsets, experts, slots, top_k, rows, qt, cap, scales, err);
 }

@@ -346,7 +346,7 @@ muon_status_t muon_fp8_quantize_cols(muon_handle_t h, int64_t x_rows, int32_t hi
     return fail(MUON_ERR_INVALID_ARG, "x is too large for one call");
   if (slots != nullptr && (top_k < 1 || top_k > muon::kMoeMaxTopK))
     return fail(MUON_ERR_INVALID_ARG, "top_k must be 1..%d (got %d)", muon::kMoeMaxTopK, top_k);
-  if (rows == 0 || capacity == 0) return MUON_OK;
+  if (rows == 0) return MUON_OK;
   MUON_TRY(check_buffers<5>({{x, x_rows * hidden * 2, false},
                              {offsets, (int64_t(experts) + 1) * 4, false},
                              {slots, slots != nullptr ? rows * 4 : 0, false},
@@ -395,8 +395,8 @@ muon_status_t muon_fp8_grouped_wgrad(muon_handle_t h, int32_t experts, int32_t n
   MUON_TRY(check_rows(capacity));
   MUON_TRY(check_hidden("n", n));
   MUON_TRY(check_hidden("k", k));
-  if (capacity < kFp8Block || capacity % kFp8Block != 0)
-    return fail(MUON_ERR_INVALID_ARG, "capacity must be a positive multiple of 128");
+  if (capacity % kFp8Block != 0)
+    return fail(MUON_ERR_INVALID_ARG, "capacity must be a multiple of 128");
   MUON_TRY(check_buffers<6>({{yt, capacity * n, false},
                              {yt_scales, capacity / kFp8Block * n, false},
                              {xt, capacity * k, false},
