@@ -530,7 +530,8 @@ muon_status_t muon_moe_combine_backward(muon_handle_t handle, int64_t tokens, in
  * written to the rows pos[t][j] >= 0 of q and scales (`rows` of them).
  * live_rows: NULL, or one int32 on the device (offsets + experts, say; 4-byte
  * aligned, outside q and scales): only
- * that many first rows of x are read and written, whatever the others hold. */
+ * that many first rows of x are read and written, whatever the others hold
+ * (with pos they are tokens, which muon_moe_plan's offsets do not count). */
 muon_status_t muon_fp8_quantize_rows(muon_handle_t handle, int64_t tokens, int32_t hidden,
                                      const uint16_t* x, const int32_t* pos, int32_t top_k,
                                      int64_t rows, const int32_t* live_rows, uint8_t* q,

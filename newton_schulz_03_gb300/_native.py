@@ -555,7 +555,8 @@ def muon_fp8_quantize_rows(handle: int, x, q, scales, pos=None, offsets=None,
     """Rows of ``x`` [tokens, hidden] (BF16) to e4m3 ``q`` with a scale byte
     (E8M0) per 128; with ``pos`` [tokens, k], row t goes to rows pos[t].  With
     ``offsets`` (muon_moe_plan's) only the rows of some expert, the first
-    offsets[-1], are read and written."""
+    offsets[-1], are read and written.  They count rows, which tokens sent by
+    ``pos`` are not: one or the other."""
     (t, d), r = x.shape, q.shape[0]
     k = 0
     if pos is not None:
@@ -564,6 +565,8 @@ def muon_fp8_quantize_rows(handle: int, x, q, scales, pos=None, offsets=None,
         raise ValueError(f"q must have {t} rows, got {r}")
     live = 0
     if offsets is not None:
+        if pos is not None:
+            raise ValueError("offsets count rows and do not go with pos")
         if offsets.numel() == 0:
             raise ValueError("offsets must not be empty")
         live = _want("offsets", offsets, None, "i32") + 4 * (offsets.numel() - 1)

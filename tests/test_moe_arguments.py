@@ -87,3 +87,13 @@ def test_the_mask_is_not_an_output(ns, h):
     ns.muon_moe_route(h, x, ids, w, mask=mask[3:])
     assert (ids[0] == -1).all() and (ids[1:] >= 0).all()
     ns.muon_last_device_error(h)
+
+
+def test_offsets_do_not_go_with_pos(ns):
+    """They count rows: as a count of tokens they would leave out the tokens
+    past the number of rows, though these have rows of their own."""
+    x = torch.zeros(4, 32, dtype=torch.bfloat16)
+    q, s = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 1, dtype=torch.uint8)
+    pos = torch.tensor([[-1], [-1], [-1], [0]], dtype=torch.int32)
+    with pytest.raises(ValueError, match="do not go with pos"):
+        ns.muon_fp8_quantize_rows(1, x, q, s, pos=pos, offsets=torch.tensor([0, 1], dtype=torch.int32))
