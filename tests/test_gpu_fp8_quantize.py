@@ -319,3 +319,38 @@ def test_refusals(ns, h):
     with pytest.raises(ValueError):
         ns.muon_fp8_quantize_rows(h, x.float(), torch.zeros(4, 32, dtype=torch.uint8, device="cuda"),
                                   torch.zeros(4, 1, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_nonfinite_weights_of_either_type(ns, h, dtype):
+    """NaN and infinities in blocks of their own and together: the scale is the
+    finite values', or the largest one where an infinity is; all else as ever."""
+    w = (torch.randn(2, 272, 400, generator=torch.Generator("cuda").manual_seed(8), device="cuda") * 3).to(getattr(torch, dtype))
+    places = [(0, 0, 0, "nan"), (0, 127, 127, "nan"), (0, 200, 140, "inf"), (0, 271, 399, "-inf"), (1, 5, 6, "nan"), (1, 7, 8, "-inf"),
+              (1, 260, 300, "nan"), (1, 261, 303, "-nan")]
+    for e, r, c, v in places:
+        w[e, r, c] = float(v.replace("-nan", "nan")) * (-1 if v == "-nan" else 1)
+    q, qt = torch.empty(2, 272, 400, dtype=torch.uint8, device="cuda"), torch.empty(2, 400, 272, dtype=torch.uint8, device="cuda")
+    s, st = torch.empty(2, 3, 4, dtype=torch.uint8, device="cuda"), torch.empty(2, 4, 3, dtype=torch.uint8, device="cuda")
+    ns.muon_fp8_quantize_blocks(h, w, q, s, qt, st)
+    with pytest.raises(ns.MuonError) as ei:
+        ns.muon_last_device_error(h)
+    assert ei.value.status_name == "MUON_ERR_NONFINITE"
+    want, ws = ref.quantize_blocks(finite_reference(w.double().cpu().numpy()))
+    np.testing.assert_array_equal(s.cpu().numpy(), ws)
+    assert torch.equal(qt, q.transpose(1, 2)) and torch.equal(st, s.transpose(1, 2))
+    ok = np.ones(want.shape, dtype=bool)
+    for e, r, c, v in places:
+        ok[e, r, c] = False
+        if v.endswith("nan"):
+            assert int(q[e, r, c]) & 0x7F == 0x7F
+        else:
+            assert int(q[e, r, c]) == (0xFE if v == "-inf" else 0x7E)
+    np.testing.assert_array_equal(q_of(q.view(F8))[ok], want[ok])
+    # A block of nothing but NaN has no magnitude: scale 1.
+    w = torch.full((1, 16, 16), float("nan"), dtype=w.dtype, device="cuda")
+    q, s = torch.empty(1, 16, 16, dtype=torch.uint8, device="cuda"), torch.empty(1, 1, 1, dtype=torch.uint8, device="cuda")
+    ns.muon_fp8_quantize_blocks(h, w, q, s)
+    assert int(s) == 127 and ((q & 0x7F) == 0x7F).all()
+    with pytest.raises(ns.MuonError):
+        ns.muon_last_device_error(h)
