@@ -30,11 +30,14 @@
 // counts before its first tile, so a call needs no host copy of the routing.
 //
 // Bound and measured (GB300).  Rows with few tokens per expert: reading w, 512
-// experts of 1536 x 4096 with 57344 rows 531-547 us (3.63 GB, 6.6-6.8 TB/s).
-// Dense: the tensor pipe at the power cap, 16381 x 6144 x 4096 240-280 us
-// (2.9-3.4 PFLOP/s, pipe 88% active).  One token through 7 experts: latency,
-// 14-15 us.  Weight gradient with few tokens per expert: writing dw, 64 experts
-// of 2048 x 8704 725-765 us (4.66 GB, 6.1-6.4 TB/s).
+// experts of 1536 x 4096 with 57344 rows 531-550 us (3.63 GB, 6.6-6.8 TB/s).
+// Dense: the tensor pipe at the power cap, 16381 x 6144 x 4096 280 us in a stream
+// of calls (2.9 PFLOP/s), 240 us by itself (3.4 PFLOP/s, pipe 89% active).  One
+// token through 7 experts: latency, 15.1-15.5 us.  Weight gradient with few tokens
+// per expert: writing dw, 64 experts of 2048 x 8704 725-765 us (4.66 GB, 6.1-6.4
+// TB/s), added to what is there 1840 us (floor 1356).  With one expert the tiles
+// are few: 16384 rows into 6144 x 4096 261 us (floor 217), but into 1024 x 1024
+// 50 us (floor 9) and 4096 x 272 54 us (floor 11).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -57,7 +60,9 @@ constexpr int kSetBlocks = 4;                     // K blocks per set of scales
 constexpr int kScaleBytes = 512 + 1024;           // per set: 128 A cells, 256 B cells
 constexpr int kMaxTokens = 224;                   // rows: widest token tile
 constexpr int kWidthUnit = 32;                    // MMA columns come in multiples of this
-constexpr int kGradN = 224;                       // wgrad: columns per tile (a multiple of 32)
+constexpr int kGradN = 224;                       // wgrad: columns per tile (a multiple of 32), the
+                                                  // last one's too: 0.4% idle at k = 8704, 4% at
+                                                  // 4096, 9% at 1024, 39% at 272
 constexpr int kTokenGroup = 8;                    // rows: token tiles that share a sweep over w
 constexpr int kTmemCols = 512;
 constexpr int kTmemScales = 448;
@@ -826,9 +831,16 @@ cudaError_t launch_fp8_grouped_wgrad(const uint8_t* yt, const uint8_t* yt_scales
   p.tiles_n = (k + kGradN - 1) / kGradN;
   // Few K blocks per expert: writing dw bounds the call, and pairs that load no
   // further than the next tile stay together, so that neighbouring tiles' rows
-  // leave L2 as whole runs.  Measured with 2 stages and scale warps / 5 and 4:
-  // 2.0 blocks per expert (2048 x 8704 x 64) 726 / 832 us; 3.5 (1536 x 4096 x 64)
-  // 379 / 315 us; 32 (2048 x 8704 x 8) 727 / 403 us (2.9 PFLOP/s).
+  // leave L2 as whole runs.  Measured with 2 stages and scale warps / 5 and 4, by
+  // blocks of capacity per expert (us):
+  //                        1.5         2.5         3.0         3.5         5.0
+  //   64 x 2048 x 8704   810/822     740/894     806/918     890/924    1135/904
+  //   64 x 1536 x 4096   294/298     287/324     326/329     355/337     449/316
+  //   512 x 1536 x 4096 2471/2544   2205/2827   2492/2931   2851/3041   3532/3090
+  //   256 x 256 x 1024    64/64       74/74       85/76       95/81      111/89
+  //   64 x 512 x 512      23/25       31/27       36/31       36/29       40/33
+  // The two cross between 2.5 and 4.5, the earlier the smaller dw is; where dw
+  // fits L2 they differ by a few us.  8 x 2048 x 8704 at 32: 727/403.
   const bool few = 2 * (cap / kBK) < 5 * static_cast<int64_t>(experts);
   p.stages = few ? 2 : Layout<true>::kStages;
   p.scale_warps = few ? 2 : Layout<true>::kScaleWarps;

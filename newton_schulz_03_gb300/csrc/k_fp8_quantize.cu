@@ -19,8 +19,8 @@
 // through the device error word.  Each value is read once and written as one
 // byte (two with the transpose): rows and blocks are bound by HBM (8192 tokens x
 // 4096 to 7 rows each 46.5 us, 6.5 TB/s; 48 FP32 weights of 2048 x 8704 in both
-// orientations 756 us, 6.8 TB/s), cols by its instructions (8191 x 4096 gathered
-// into 512 experts 109 us, 2.8 TB/s).
+// orientations 759 us, 6.8 TB/s), cols by its two barriers per tile and its
+// instructions (8191 x 4096 gathered into 512 experts 110 us, 2.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -276,10 +276,10 @@ __global__ void __launch_bounds__(kTileThreads) quantize_blocks_kernel(
   }
 }
 
-// BF16 weights: magnitudes and scaling on pairs, as the column quantiser; four
-// blocks per SM.  With the FP32 kernel's arithmetic on converted values the
-// instructions bound it: 48 x 2048 x 4096 414 us, this one 233 us (the measured
-// copy bandwidth).
+// BF16 weights: magnitudes and scaling on pairs, as the column quantiser; three
+// blocks per SM (80 registers).  With the FP32 kernel's arithmetic on converted values the
+// instructions bound it: 48 x 2048 x 4096 414 us, this one 235-238 us (the
+// measured copy bandwidth).
 __global__ void __launch_bounds__(kTileThreads, 3) quantize_blocks_bf16_kernel(
     const uint16_t* __restrict__ w, int n, int k, uint8_t* __restrict__ q,
     uint8_t* __restrict__ scales, uint8_t* __restrict__ qt, uint8_t* __restrict__ scales_t,
@@ -346,12 +346,13 @@ __global__ void __launch_bounds__(kTileThreads, 3) quantize_blocks_bf16_kernel(
 // ------------------------------------------------------------------ columns
 // Persistent blocks over (chunk of kStripes 128-column stripes, block of 128
 // rows of one expert), all row blocks of a chunk before the next chunk's: the
-// gathered rows of a chunk (tokens x 1 KB) stay in L2 while the token's other
+// gathered rows of a chunk (tokens x 2 KB) stay in L2 while the token's other
 // experts read them, and a row block looks up its rows once per chunk.  The next
 // stripe's loads are in flight while a stripe is written.
 // Magnitudes are compared as pairs of 16-bit integers and values scaled by
-// mixed-precision FMAs that take BF16 halves in place: the kernel is bound by
-// its instructions, not by memory.
+// mixed-precision FMAs that take BF16 halves in place.  Not memory holds the
+// kernel but its two barriers per stripe (the largest stall, with three blocks
+// per SM at 75 registers) and its instructions (issue slots 59% busy).
 constexpr int kStripes = 8;
 constexpr uint32_t kNoRow = 0xffffffffu;
 

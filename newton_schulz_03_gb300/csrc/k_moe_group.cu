@@ -12,7 +12,9 @@
 // serving case, where a launch costs as much as the work.  Bound by latency: Q
 // is the least of 1, 2, 4, 8 that keeps to 128 chunks, whose histograms a thread
 // sums sixteen loads at a time.  57337 slots over 512 experts take 8.2 us (14
-// chunks of 4096: 12.7 us), 458752 slots 16 us, 259 slots 2.4 us.
+// chunks of 4096: 12.7 us), 458752 slots 16 us, 259 slots 2.4 us.  Past 2^20 slots
+// there are more than 128 chunks, and their sums cost the square of the number:
+// 2^20 slots 31 us from a cold cache, 2^22 132 us, 2^24 0.9 ms, 2^26 11 ms.
 //
 // Combine: out[t] = sum_j w[t][j] y[pos[t][j]], FP32 sums in the order of j,
 // rounded once.  Backward: grad_y[pos[t][j]] = w[t][j] grad_out[t] and

@@ -15,11 +15,13 @@
 // them would cost a write and a read of tokens x experts.
 //
 // One warp holds one token's logits in registers.  The logits are read once and
-// their gradient written once; the forward pass is bound by its instructions
-// (500-1200 per token and warp: a look at every value, then the few candidates),
-// the backward pass by HBM, one token by latency.  Measured: 16384 x 512 FP32
-// softmax 12 us forward, 13 us backward (floors 5 and 10); 65531 x 512 BF16
-// sigmoid with 16 groups 77 and 21 us (floors 10 and 11); one token 2.7 us.
+// their gradient written once.  Measured: 16384 x 512 FP32 softmax 12 us forward,
+// 13 us backward (floors 5 and 10); 65531 x 512 BF16 sigmoid with 16 groups 77 and
+// 21 us (floors 10 and 11); one token 2.7 us.  What holds them: forward, the
+// instructions of a warp per token (620 softmax, 1200 with groups: a look at every
+// value, then the few candidates) and their latencies, issue slots 67% and 81%
+// busy; backward, one chain of dependent loads per token (ids, logits, score,
+// store), slots 60% busy, most stalls on those loads; one token, latency.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
