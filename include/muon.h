@@ -140,7 +140,9 @@ const char* muon_version(void);
  * (0 = default of 8 GiB); groups whose whole batch does not fit are
  * processed in chunks (a single matrix always gets room).  The scratch of
  * muon_moe_plan is apart from it, and all of it together within the same
- * cap: a grouping that needs more is refused (NOMEM).  No device memory is allocated until first use.
+ * cap: a grouping that needs more is refused (NOMEM).  A call that needs a
+ * larger workspace frees the one before it, and with it ends the use of
+ * captured graphs of the step's calls (not of the grouping's).  No device memory is allocated until first use.
  * Errors: INVALID_ARG (out == NULL), NO_DEVICE, UNSUPPORTED_ARCH (not
  * sm_103), CUDA. */
 muon_status_t muon_create(muon_handle_t* out, int32_t device, size_t workspace_bytes_max);
