@@ -377,8 +377,13 @@ int handle_scratch(muon_handle_s* h, size_t bytes, void** out) {
     const size_t want = std::min(std::max(least, align_up(bytes, kAlign)), room);
     constexpr int kMost = sizeof(h->scratch) / sizeof(h->scratch[0]);
     if (h->n_scratch == kMost) return fail(MUON_ERR_NOMEM, "the handle's scratch has grown %d times", kMost);
+    // A call that is being captured may be the handle's first: the allocation is
+    // no work of the stream, and this mode lets it pass.
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
     void* p = nullptr;
     const cudaError_t e = cudaMalloc(&p, want);
+    cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) {
       cudaGetLastError();
       return fail(MUON_ERR_NOMEM, "scratch allocation of %zu bytes failed: %s", want,

@@ -117,3 +117,26 @@ def test_scratch_keeps_to_the_cap(ns):
         with pytest.raises(ns.MuonError):
             call(h, 4 << 20)                              # 2 MiB are more than what is left
         call(h, 3 << 20)                                  # 1.5 MiB are not: all that is left
+
+
+@pytest.mark.parametrize("stepped", [False, True])
+def test_the_first_grouping_may_be_a_captured_one(ns, stepped):
+    """Scratch is taken during the capture where the handle has none yet."""
+    n, experts = 8000, 512
+    with ns.Handle() as h:
+        if stepped:
+            w, mo, g = (torch.randn(2, 128, 256, device="cuda") for _ in range(3))
+            ns.muon_step(h.value, [(128, 256, 2)], [mo], [g], [w], 0.02, 0.0, 0.9)
+        ids, out = random_ids(n, experts, 0).cuda(), buffers(n, experts)
+        torch.cuda.synchronize()
+        graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=s):
+            ns.muon_moe_plan(h.value, ids, *out)
+        for seed in (1, 2):
+            fresh = random_ids(n, experts, seed)
+            ids.copy_(fresh)
+            graph.replay()
+            torch.cuda.synchronize()
+            for got, want in zip(out, ref.plan(fresh.numpy(), experts)):
+                np.testing.assert_array_equal(got.cpu().numpy(), want)
+        ns.muon_last_device_error(h.value)
