@@ -743,6 +743,14 @@ muon_status_t muon_policy_loss_backward(muon_handle_t handle, int64_t tokens, in
  * Errors: INVALID_ARG (limit out of range), CUDA. */
 muon_status_t muon_selftest_bounded_wait(muon_handle_t handle, int32_t limit_ms, void* stream);
 
+/* The same of the losses that stream rows (loss and gradient in one call, two rows
+ * and more for every block): in the handle's next such call nothing brings a
+ * block's logits (`what` 1), or what else a row needs (2), after its first row.
+ * The waits give up after 2 seconds, the rows that were complete stay, no other is
+ * written, and muon_last_device_error() reports MUON_ERR_TIMEOUT.  A call of few rows
+ * takes the request off and runs as ever.  Errors: INVALID_ARG. */
+muon_status_t muon_selftest_loss_wait(muon_handle_t handle, int32_t what);
+
 /* Per-kernel timing: when enabled, every launch is bracketed by CUDA
  * events on the launching stream.  muon_kernel_stats synchronises the
  * device, folds the recorded events into `out` and keeps accumulating;

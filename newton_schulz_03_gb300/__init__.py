@@ -21,7 +21,7 @@ from ._native import (  # noqa: F401
     muon_moe_route, muon_moe_route_backward, KERNEL_CLASSES, muon_distill_loss,
     muon_distill_loss_backward, muon_kernel_class_stats, muon_policy_loss,
     muon_policy_loss_backward, GATE_GELU, GATE_RELU, GATE_SILU, muon_gated_fp8_backward,
-    muon_gated_fp8_matmul, muon_gated_fp8_matmul_sum,
+    muon_gated_fp8_matmul, muon_gated_fp8_matmul_sum, muon_selftest_loss_wait,
 )
 
 __all__ = [
@@ -44,5 +44,5 @@ __all__ = [
     "KERNEL_CLASSES", "muon_kernel_class_stats", "muon_distill_loss",
     "muon_distill_loss_backward", "muon_policy_loss", "muon_policy_loss_backward",
     "GATE_SILU", "GATE_GELU", "GATE_RELU", "muon_gated_fp8_matmul", "muon_gated_fp8_backward",
-    "muon_gated_fp8_matmul_sum",
+    "muon_gated_fp8_matmul_sum", "muon_selftest_loss_wait",
 ]

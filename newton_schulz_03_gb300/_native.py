@@ -41,7 +41,7 @@ EXPORTED = (
     "muon_fp8_quantize_cols", "muon_fp8_grouped_matmul", "muon_fp8_grouped_wgrad",
     "muon_distill_loss", "muon_distill_loss_backward", "muon_policy_loss",
     "muon_policy_loss_backward", "muon_kernel_class_stats", "muon_gated_fp8_matmul",
-    "muon_gated_fp8_backward", "muon_gated_fp8_matmul_sum",
+    "muon_gated_fp8_backward", "muon_gated_fp8_matmul_sum", "muon_selftest_loss_wait",
 )
 # Classes that muon_kernel_class_stats alone knows.
 KERNEL_CLASSES = KERNEL_NAMES + ("loss",)
@@ -196,6 +196,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                               c_vp, c_vp, c_vp, P(_PolicyOptions), c_vp, c_vp,
                                               c_vp, c_vp, c_i64, c_vp]),
         "muon_kernel_class_stats": (c_int, [c_vp, c_i32, P(ctypes.c_double), P(c_i64)]),
+        "muon_selftest_loss_wait": (c_int, [c_vp, c_i32]),
         "muon_set_kernel_timing": (c_int, [c_vp, c_i32]),
         "muon_kernel_stats": (c_int, [c_vp, P(_StatsV1)]),
         "muon_kernel_stats_v2": (c_int, [c_vp, P(_Stats)]),
@@ -844,6 +845,13 @@ def muon_selftest_bounded_wait(handle: int, limit_ms: int = 50, stream=None) -> 
     """Launch the bounded-wait self-test; muon_last_device_error then
     raises MUON_ERR_TIMEOUT."""
     _check(load_library().muon_selftest_bounded_wait(handle, limit_ms, _stream(stream)))
+
+
+def muon_selftest_loss_wait(handle: int, what: int) -> None:
+    """In the handle's next loss with gradient of many rows nothing brings the
+    logits (1), or what else a row needs (2), after each block's first row: the
+    waits run out, muon_last_device_error raises MUON_ERR_TIMEOUT."""
+    _check(load_library().muon_selftest_loss_wait(handle, what))
 
 
 def muon_set_kernel_timing(handle: int, enable: bool) -> None:

@@ -26,6 +26,9 @@ int handle_info(muon_handle_s* h, HandleInfo* out);
 // the handle goes, since a captured graph may still write to it.
 int handle_scratch(muon_handle_s* h, size_t bytes, void** out);
 
+// What muon_selftest_loss_wait asked of this call, which takes it off.
+int take_loss_stall(muon_handle_s* h);
+
 // Counts one kernel launch of class `kind` and, with timing on, brackets it
 // with events.
 class LaunchMark {

@@ -790,6 +790,8 @@ __global__ void __launch_bounds__(kStreamBound, 1)
     return l.mask != 0 && l.action >= 0 && l.action < a.vocab;
   };
   int n_rows = (tokens - static_cast<int>(blockIdx.x) + step - 1) / step, n_rest = 0;
+  // Rows that a loading warp brings: all, but for the self-test of the waits.
+  const auto brought = [&](int stalled) { return a.stall == stalled ? min(n_rows, 1) : n_rows; };
   if (listed) {
     // Each warp a range of tokens, 32 to a word (kept in the ring, still unused).
     uint32_t* words = reinterpret_cast<uint32_t*>(dyn);
@@ -843,7 +845,7 @@ __global__ void __launch_bounds__(kStreamBound, 1)
       int64_t issued = 0;
       bool ok = true;
       Look here = look(nth(0)), next = look(nth(1));
-      for (int i = 0; ok && i < n_rows; ++i) {
+      for (int i = 0; ok && i < brought(kLossStallLogits); ++i) {
         const int tok = nth(i);
         const Look after = look(nth(i + 2));
         if (counts(here)) {
@@ -887,7 +889,7 @@ __global__ void __launch_bounds__(kStreamBound, 1)
     int turn = 0;
     uint32_t phase = 0;
     Look here = look(nth(0)), next = look(nth(1));
-    for (int i = 0; i < n_rows; ++i) {
+    for (int i = 0; i < brought(kLossStallTargets); ++i) {
       const int tok = nth(i), action = here.action;
       const Look after = look(nth(i + 2));
       const bool live = counts(here);
@@ -1043,11 +1045,28 @@ __global__ void __launch_bounds__(kStreamBound, 1)
     }
   } else {
     // ------------------------------------------------------------ the rows
-    // Waits that run out leave garbage, reported, and every barrier met.
+    // A wait that runs out is reported, and ends the rows.  Every warp meets the others
+    // once per row, whatever it has seen of it, and all of them go on or none: only what
+    // has arrived for all is an index or decides on a branch that they take together.
+    bool arrived = true;                            // every wait of this thread
     const auto expect = [&](uint64_t* bar, uint32_t phase) {
-      if (!ptx::mbar_wait(bar, phase, abort)) give_up();
+      if (!ptx::mbar_wait(bar, phase, abort)) {
+        give_up();
+        arrived = false;
+      }
     };
-    const auto meet_rows = [&] { asm volatile("barrier.cta.sync.aligned 1, %0;" ::"r"(nthr) : "memory"); };
+    const auto meet_rows = [&](bool ok) {
+      uint32_t all_ok;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\t"
+          "setp.ne.b32 p, %2, 0;\n\t"
+          "barrier.cta.red.and.aligned.pred q, 1, %1, p;\n\t"
+          "selp.b32 %0, 1, 0, q;\n\t}"
+          : "=r"(all_ok)
+          : "r"(nthr), "r"(ok ? 1u : 0u)
+          : "memory");
+      return all_ok != 0;
+    };
     // What was read has been used: nothing to wait for.  (An arrival that releases
     // memory would wait for the gradient's stores in flight.)
     const auto release = [&](uint64_t* bar) {
@@ -1099,7 +1118,8 @@ __global__ void __launch_bounds__(kStreamBound, 1)
       const int chunks = (row.full + span - 1) / span;
       const int again = max(chunks - keep, 0);
       const int edge = tid < row.edges ? row.edge<N>(tid) : -1;
-      const bool live = m.live != 0;
+      // (the same in all of a warp: it stays converged)
+      const bool live = __all_sync(kAll, arrived) && m.live != 0;
       const Stat teacher = m.teacher;
       const bool counted = live && (KIND == kPolicy || teacher.ref > -INFINITY);
       uint4 d[PT];
@@ -1181,7 +1201,9 @@ __global__ void __launch_bounds__(kStreamBound, 1)
       if (counted) {
         mine.sum = warp_sum(mine.sum);
         if (lane == 0) sh.part[swap][warp] = mine;
-        meet_rows();
+      }
+      if (!meet_rows(arrived)) break;
+      if (counted) {
         all = join_all(sh.part[swap], warps, lane, c);
         finish(swap ^ 1);
         ln_all = ln_sum(all, c);
@@ -1302,7 +1324,7 @@ __global__ void __launch_bounds__(kStreamBound, 1)
       if (turn == 0) meta_phase ^= 1u;
     }
     if (KIND == kDistill) {
-      meet_rows();
+      meet_rows(true);
       finish(swap ^ 1);
     }
     for (int i = 0; i < n_rest; ++i) {

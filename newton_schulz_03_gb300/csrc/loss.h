@@ -12,6 +12,10 @@ constexpr int kLossMaxTargets = 1024;              // teacher's logits per token
 constexpr int32_t kLossMaxVocab = 1 << 24;
 constexpr int64_t kLossMaxTokens = int64_t(1) << 27;   // tokens x cluster is a grid's x
 
+// Self-test of the waits, where rows are streamed: after each block's first row
+// nothing brings the logits, or what else a row needs.
+enum LossStall : int32_t { kLossStallNone = 0, kLossStallLogits = 1, kLossStallTargets = 2 };
+
 struct LossArgs {
   const void* logits;          // [tokens], `ld` elements apart
   int64_t ld;
@@ -39,6 +43,7 @@ struct LossArgs {
   float ratio_low, ratio_high; // 1 - clip_low, 1 + clip_high
   float kl_coef;
   int* err;
+  int32_t stall;               // LossStall
 };
 
 // Shared-memory attributes of the kernels (called when a handle is made, with its

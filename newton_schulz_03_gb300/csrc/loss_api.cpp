@@ -103,6 +103,7 @@ muon_status_t distill(muon_handle_t h, int64_t tokens, int32_t vocab, const void
        {lse, tokens * 4, !backward, 4},
        {grad_loss, grad ? tokens * 4 : 0, false, 4},
        {grad_logits, grad ? extent(tokens, vocab, grad_ld, el) : 0, true, static_cast<int>(el)}}));
+  if (grad && !backward) a.stall = muon::take_loss_stall(h);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   muon::LaunchMark mark(h, MUON_KERNEL_LOSS, s);
   return launched(muon::launch_distill_loss(a, logits_type == MUON_BF16, grad, backward, hi.num_sms, s),
@@ -164,6 +165,7 @@ muon_status_t policy(muon_handle_t h, int64_t tokens, int32_t vocab, const void*
        {lse, tokens * 4, !backward, 4},
        {grad_loss, grad ? tokens * 4 : 0, false, 4},
        {grad_logits, grad ? extent(tokens, vocab, grad_ld, el) : 0, true, static_cast<int>(el)}}));
+  if (grad && !backward) a.stall = muon::take_loss_stall(h);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   muon::LaunchMark mark(h, MUON_KERNEL_LOSS, s);
   return launched(muon::launch_policy_loss(a, logits_type == MUON_BF16, grad, backward, hi.num_sms, s),

@@ -204,6 +204,7 @@ struct muon_handle_s {
   void* ws = nullptr;
   size_t ws_size = 0;
   int* dev_err = nullptr;
+  int loss_stall = muon::kLossStallNone;    // of the next loss with gradient
   // Scratch of the grouping: the last one is in use, none is freed before the
   // handle (captured graphs hold their addresses).
   struct Scratch {
@@ -381,6 +382,12 @@ int handle_info(muon_handle_s* h, HandleInfo* out) {
   out->fp8_pairs = h->fp8_pairs;
   out->dev_err = h->dev_err;
   return MUON_OK;
+}
+
+int take_loss_stall(muon_handle_s* h) {
+  const int what = h->loss_stall;
+  h->loss_stall = kLossStallNone;
+  return what;
 }
 
 int handle_scratch(muon_handle_s* h, size_t bytes, void** out) {
@@ -1228,6 +1235,15 @@ muon_status_t muon_selftest_bounded_wait(muon_handle_t h, int32_t limit_ms, void
   cudaError_t e = muon::launch_bounded_wait_selftest(
       h->dev_err, static_cast<uint64_t>(limit_ms) * 1000000ull, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "self-test launch");
+  return MUON_OK;
+}
+
+muon_status_t muon_selftest_loss_wait(muon_handle_t h, int32_t what) {
+  muon_status_t st = check_handle(h);
+  if (st != MUON_OK) return st;
+  if (what != muon::kLossStallLogits && what != muon::kLossStallTargets)
+    return fail(MUON_ERR_INVALID_ARG, "what must be 1 or 2 (got %d)", what);
+  h->loss_stall = what;
   return MUON_OK;
 }
 
