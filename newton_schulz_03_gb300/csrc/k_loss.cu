@@ -714,6 +714,7 @@ struct StreamShared {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t meta_full[2], meta_empty[2];
   int abort;
+  int late[2];                            // a computing warp's wait has run out
   int ranks[kStreamBound / 32];            // counts of the warps
   struct {
     int live, action;
@@ -766,7 +767,7 @@ __global__ void __launch_bounds__(kStreamBound, 1)
       ptx::mbar_init(&sh.meta_full[i], 1);
       ptx::mbar_init(&sh.meta_empty[i], static_cast<uint32_t>(warps));
     }
-    sh.abort = 0;
+    sh.abort = sh.late[0] = sh.late[1] = 0;
     ptx::fence_barrier_init();
   }
   __syncthreads();
@@ -790,8 +791,6 @@ __global__ void __launch_bounds__(kStreamBound, 1)
     return l.mask != 0 && l.action >= 0 && l.action < a.vocab;
   };
   int n_rows = (tokens - static_cast<int>(blockIdx.x) + step - 1) / step, n_rest = 0;
-  // Rows that a loading warp brings: all, but for the self-test of the waits.
-  const auto brought = [&](int stalled) { return a.stall == stalled ? min(n_rows, 1) : n_rows; };
   if (listed) {
     // Each warp a range of tokens, 32 to a word (kept in the ring, still unused).
     uint32_t* words = reinterpret_cast<uint32_t*>(dyn);
@@ -840,12 +839,13 @@ __global__ void __launch_bounds__(kStreamBound, 1)
   if (warp == warps) {
     // ------------------------------------------------------------ chunks
     if (lane == 0) {
+      if (a.stall == kLossStallLogits) n_rows = min(n_rows, 1);     // (self-test of the waits)
       int slot = 0;
       uint32_t phase = 0;
       int64_t issued = 0;
       bool ok = true;
       Look here = look(nth(0)), next = look(nth(1));
-      for (int i = 0; ok && i < brought(kLossStallLogits); ++i) {
+      for (int i = 0; ok && i < n_rows; ++i) {
         const int tok = nth(i);
         const Look after = look(nth(i + 2));
         if (counts(here)) {
@@ -886,10 +886,11 @@ __global__ void __launch_bounds__(kStreamBound, 1)
     }
   } else if (warp == warps + 1) {
     // ------------------------------------------------------------ the rest of a row
+    if (a.stall == kLossStallTargets) n_rows = min(n_rows, 1);
     int turn = 0;
     uint32_t phase = 0;
     Look here = look(nth(0)), next = look(nth(1));
-    for (int i = 0; i < brought(kLossStallTargets); ++i) {
+    for (int i = 0; i < n_rows; ++i) {
       const int tok = nth(i), action = here.action;
       const Look after = look(nth(i + 2));
       const bool live = counts(here);
@@ -1045,27 +1046,25 @@ __global__ void __launch_bounds__(kStreamBound, 1)
     }
   } else {
     // ------------------------------------------------------------ the rows
-    // A wait that runs out is reported, and ends the rows.  Every warp meets the others
-    // once per row, whatever it has seen of it, and all of them go on or none: only what
-    // has arrived for all is an index or decides on a branch that they take together.
-    bool arrived = true;                            // every wait of this thread
-    const auto expect = [&](uint64_t* bar, uint32_t phase) {
-      if (!ptx::mbar_wait(bar, phase, abort)) {
-        give_up();
-        arrived = false;
-      }
+    // A wait that runs out is reported, and ends the rows for all warps together.  They
+    // meet once per row that counts and at the end; a warp whose targets have not come
+    // does not know whether its row counts: it reads nothing of it, goes to the next
+    // meeting at once and leaves.  late[meeting] is written before that meeting and read
+    // after it, and its place used again two meetings later.
+    int meeting = 0;
+    bool left = false;
+    const auto miss = [&] {
+      give_up();
+      sh.late[meeting] = 1;
     };
-    const auto meet_rows = [&](bool ok) {
-      uint32_t all_ok;
-      asm volatile(
-          "{\n\t.reg .pred p, q;\n\t"
-          "setp.ne.b32 p, %2, 0;\n\t"
-          "barrier.cta.red.and.aligned.pred q, 1, %1, p;\n\t"
-          "selp.b32 %0, 1, 0, q;\n\t}"
-          : "=r"(all_ok)
-          : "r"(nthr), "r"(ok ? 1u : 0u)
-          : "memory");
-      return all_ok != 0;
+    const auto expect = [&](uint64_t* bar, uint32_t phase) {
+      if (!ptx::mbar_wait(bar, phase, abort)) miss();
+    };
+    const auto meet_rows = [&] {                    // whether a wait has run out
+      asm volatile("barrier.cta.sync.aligned 1, %0;" ::"r"(nthr) : "memory");
+      const int late = *const_cast<const volatile int*>(&sh.late[meeting]);
+      meeting ^= 1;
+      return late != 0;
     };
     // What was read has been used: nothing to wait for.  (An arrival that releases
     // memory would wait for the gradient's stores in flight.)
@@ -1109,7 +1108,13 @@ __global__ void __launch_bounds__(kStreamBound, 1)
     };
     for (int i = 0; i < n_rows; ++i) {
       const int tok = nth(i);
-      expect(&sh.meta_full[turn], meta_phase);
+      // (one outcome in all of a warp: it stays converged)
+      if (!__all_sync(kAll, ptx::mbar_wait(&sh.meta_full[turn], meta_phase, abort))) {
+        miss();
+        meet_rows();
+        left = true;
+        break;
+      }
       const auto& m = sh.meta[turn];
       const T* x = row_of(tok);
       T* out = static_cast<T*>(a.grad_logits) + static_cast<int64_t>(tok) * a.grad_ld;
@@ -1118,8 +1123,7 @@ __global__ void __launch_bounds__(kStreamBound, 1)
       const int chunks = (row.full + span - 1) / span;
       const int again = max(chunks - keep, 0);
       const int edge = tid < row.edges ? row.edge<N>(tid) : -1;
-      // (the same in all of a warp: it stays converged)
-      const bool live = __all_sync(kAll, arrived) && m.live != 0;
+      const bool live = m.live != 0;
       const Stat teacher = m.teacher;
       const bool counted = live && (KIND == kPolicy || teacher.ref > -INFINITY);
       uint4 d[PT];
@@ -1201,10 +1205,13 @@ __global__ void __launch_bounds__(kStreamBound, 1)
       if (counted) {
         mine.sum = warp_sum(mine.sum);
         if (lane == 0) sh.part[swap][warp] = mine;
-      }
-      if (!meet_rows(arrived)) break;
-      if (counted) {
+        // (looked at behind the parts: 65536 x 4096 BF16 262 us, at once 264)
+        const bool late = meet_rows();
         all = join_all(sh.part[swap], warps, lane, c);
+        if (late) {
+          left = true;
+          break;
+        }
         finish(swap ^ 1);
         ln_all = ln_sum(all, c);
         const float lse = all.ref / a.temperature + ln_all;
@@ -1323,10 +1330,8 @@ __global__ void __launch_bounds__(kStreamBound, 1)
       turn ^= 1;
       if (turn == 0) meta_phase ^= 1u;
     }
-    if (KIND == kDistill) {
-      meet_rows(true);
-      finish(swap ^ 1);
-    }
+    if (!left) meet_rows();                         // (with a warp that leaves, or all at the end)
+    finish(swap ^ 1);
     for (int i = 0; i < n_rest; ++i) {
       const int tok = rest[i];
       leave_out(tok);
