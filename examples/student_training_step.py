@@ -58,18 +58,21 @@ class Student:
                              grad_loss=weight, grad_logits=z)
         return loss, self.backward(z, saved)
 
-    def log_probs(self, x, actions, mask=None):
+    def log_probs(self, x, actions, mask=None, temperature=1.0):
+        """Of the actions, at the temperature that they were sampled with (and ``policy`` trains at)."""
         z, _ = self.logits(x, mask)
         loss, logp, lse = (torch.empty(x.shape[0], device=x.device) for _ in range(3))
-        ns.muon_policy_loss(self.h, z, actions, torch.zeros_like(loss), loss, logp, lse, mask=mask)
+        ns.muon_policy_loss(self.h, z, actions, torch.zeros_like(loss), loss, logp, lse, mask=mask,
+                            temperature=temperature)
         return logp
 
-    def policy(self, x, actions, advantages, old_logp, ref_logp, mask=None, **options):
+    def policy(self, x, actions, advantages, old_logp, ref_logp, mask=None, temperature=1.0, **options):
+        """As distill; ``old_logp`` and ``ref_logp`` are log_probs of the same temperature."""
         z, saved = self.logits(x, mask)
         loss, logp, lse = (torch.empty(x.shape[0], device=x.device) for _ in range(3))
         weight = _weights(x.shape[0], mask, x.device)
         ns.muon_policy_loss(self.h, z, actions, advantages, loss, logp, lse, old_logp=old_logp, ref_logp=ref_logp, mask=mask,
-                            grad_loss=weight, grad_logits=z, **options)
+                            temperature=temperature, grad_loss=weight, grad_logits=z, **options)
         return loss, self.backward(z, saved)
 
 
