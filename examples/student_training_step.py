@@ -100,6 +100,7 @@ def main():
         if a.loss == "distill":
             ids = torch.randint(0, a.vocab, (a.tokens, 32), generator=g, device="cuda", dtype=torch.int32)
             teacher = torch.randn(a.tokens, 32, generator=g, device="cuda") * 2
+            mask = None
             run = lambda: student.distill(x, teacher, ids)  # noqa: E731
         else:
             actions = torch.randint(0, a.vocab, (a.tokens,), generator=g, device="cuda", dtype=torch.int32)
@@ -107,10 +108,11 @@ def main():
             mask = (torch.arange(a.tokens, device="cuda") >= a.tokens // 4).to(torch.uint8)
             old = student.log_probs(x, actions, mask)
             run = lambda: student.policy(x, actions, advantages, old, old, mask, kl_coef=0.05)  # noqa: E731
+        weight = _weights(a.tokens, mask, "cuda")
         for i in range(a.steps):
             loss, _ = run()
             student.step(0.02)
-            print(f"step {i}: loss {float(loss.mean()):.5f}")
+            print(f"step {i}: loss {float((loss * weight).sum()):.5f}")
         ns.muon_last_device_error(handle.value)
 
 
