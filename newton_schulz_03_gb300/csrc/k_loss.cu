@@ -969,27 +969,34 @@ __global__ void __launch_bounds__(kStreamBound, 1)
               sum += own[j];
             }
           teacher = {top, warp_sum(sum)};
-          // The weights of equal ids together, by chains of each bucket.
+          // The weights of equal ids together, in their order, with the first of each: 32
+          // targets at a time, the lowest of an id looks for one before them in its bucket's
+          // chain, which has the first of each id alone, and adds up its equals' weights.
+          // (4093 rows of 50257 FP32 with 1000 targets of 5 ids 1.1 ms, of as many ids 1.2;
+          // 92 and 1.5 where each target walked a chain of all.)
           for (int b = lane; b < kBuckets; b += 32) bucket[b] = -1;
           __syncwarp();
-#pragma unroll 4
-          for (int j = lane; j < a.targets; j += 32)
-            if (ids[j] >= 0) link[j] = atomicExch(&bucket[ids[j] % kBuckets], j);
-          __syncwarp();
-          for (int j = lane; j < a.targets; j += 32) {
-            if (ids[j] < 0) continue;
-            float p = 0.0f;
-            bool first = true;
-            int same = 0;
-            for (int i = bucket[ids[j] % kBuckets]; i >= 0; i = link[i])
-              if (ids[i] == ids[j]) {
-                first = first && i >= j;
-                p += own[i];
-                ++same;
-              }
-            // (chains have no order, and sums of three would have another each time)
-            if (same > 2) first = first_of(ids, teach, a.targets, j, at_top, p);
-            total[j] = first ? p : -1.0f;
+          const auto id_at = [&](int j) { return j < a.targets ? ids[j] : -1; };
+          const auto head_of = [&](int id) { return bucket + (static_cast<uint32_t>(id) * 0x9e3779b1u >> 24); };
+          int id = id_at(lane);
+          for (int j = lane; j - lane < a.targets; j += 32) {
+            const int after = id_at(j + 32);
+            int at = *head_of(id);
+            float p = id >= 0 ? own[j] : 0.0f;
+            const uint32_t equal = __match_any_sync(kAll, id);
+            const bool lowest = id >= 0 && (equal & ((1u << lane) - 1u)) == 0;
+            if (lowest) {
+              while (at >= 0 && ids[at] != id) at = link[at];
+              if (at >= 0) p += total[at];
+              for (uint32_t rest = equal & (equal - 1u); rest != 0; rest &= rest - 1)
+                p += own[j - lane + __ffs(rest) - 1];
+              total[at >= 0 ? at : j] = p;
+            }
+            if (id >= 0 && (!lowest || at >= 0)) total[j] = -1.0f;
+            __syncwarp();                           // (chains change when none is looked through)
+            if (lowest && at < 0) link[j] = atomicExch(head_of(id), j);
+            __syncwarp();
+            id = after;
           }
           // Each target to the warp that writes its element.
           if (lane < kStreamWarps) sh.count[lane] = 0;

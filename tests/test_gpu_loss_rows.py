@@ -121,3 +121,31 @@ def test_rows_between_rows_are_refused(ns, h):
     refused(ns, lambda: ns.muon_distill_loss(h, z[:, :100], teacher, ids, loss, lse, grad_loss=w, grad_logits=z[:, 100:]), "overlaps")
     refused(ns, lambda: ns.muon_policy_loss(h, z[:, :100], ids[:, 0].contiguous(), w, loss, torch.ones(6, device="cuda"), lse,
                                             grad_loss=lse.clone(), grad_logits=z[:, 100:]), "overlaps")
+
+
+def test_equal_ids_take_no_longer_than_others(ns, h):
+    """A thousand targets per row on a few entries, on one, and on entries a power of two
+    apart, in many rows: the time of a thousand different ones, not that of their pairs."""
+    t, v, k = 700, 20000, 1000
+    z, g = logits_of(t, v, BF16, 43)
+    teacher = torch.randn(t, k, generator=g, device="cuda")
+    apart = torch.rand(t, v, generator=g, device="cuda").argsort(1)[:, :k].int()
+    few = torch.randint(0, 5, (t, k), generator=g, device="cuda", dtype=torch.int32)
+    w, grad = torch.rand(t, generator=g, device="cuda"), torch.empty_like(z)
+    outs = [torch.empty(t, device="cuda") for _ in range(2)]
+
+    def took(ids):
+        best = float("inf")
+        for _ in range(4):
+            began, ended = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            began.record()
+            ns.muon_distill_loss(h, z, teacher, ids, *outs, grad_loss=w, grad_logits=grad)
+            ended.record()
+            ended.synchronize()
+            best = min(best, began.elapsed_time(ended))
+        return best
+
+    usual = took(apart)
+    for ids in (few, torch.full_like(few, 7), apart // 256 * 256):
+        assert took(ids.contiguous()) <= 4 * usual
+    ns.muon_last_device_error(h)
