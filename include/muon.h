@@ -662,12 +662,14 @@ muon_status_t muon_fp8_grouped_wgrad(muon_handle_t handle, int32_t experts, int3
  * no other buffer.  (Vectors are stored where its rows start at the same
  * place within 16 bytes as the logits', single elements otherwise.)
  *
- * A loss or lse that is not finite (a NaN or +inf among the logits or
- * targets, a target whose q is 0, a row of -inf alone) is written as it is and
- * sets the device error flag (MUON_ERR_NONFINITE); an id outside the
- * vocabulary sets it too (MUON_ERR_INVALID_ARG) and is left out.
- * Buffers are aligned to their elements; inputs and outputs must not overlap
- * but for grad_logits.  No call takes device memory.
+ * A loss or lse that is not finite is written as it is and sets the device
+ * error flag (MUON_ERR_NONFINITE): NaN where the logits or the teacher's have no
+ * softmax (a NaN or +inf among them, logits of -inf alone; the lse alone where the
+ * policy loss does not depend on it), an infinity for a target whose q is 0.  An id outside the vocabulary sets it too (MUON_ERR_INVALID_ARG) and is
+ * left out.  Buffers are aligned to their elements; inputs and outputs must not
+ * overlap but for grad_logits, where rows with a pitch count as one stretch from the
+ * first element to the last (a gradient in the gaps between the logits' rows is
+ * refused).  No call takes device memory.
  * ------------------------------------------------------------------ */
 
 /* Options of the distillation. */

@@ -295,7 +295,7 @@ __device__ __forceinline__ void meet(int id) {
 // Gate activations, two values at a time: f(x) = x s(u(x)) with s the logistic function,
 // u = x (silu) or 2 sqrt(2 / pi) (x + 0.044715 x^3) (gelu, its tanh form), or max(x, 0);
 // and f' = s + x s (1 - s) u'.  The exponential and the reciprocal are the
-// approximate instructions (2^-22 each): their result is rounded to BF16.  Past
+// approximate instructions (2^-22 and 2^-23): their result is rounded to BF16.  Past
 // |x| = 64 the logistic function is 0 or 1 in FP32 and u' has no part in f', so that
 // x^2 is taken no further there (0 x inf).  (One at a time takes half as many instructions
 // again: 16381 x 6144 x 4096 forward 486 us instead of 480, calls one after another.)

@@ -9,8 +9,9 @@
 //                 loss = -min(r A, clip(r) A) + kl (exp(d) - d - 1)
 //                 dz_v = g slope / T ([v = a] - q_v),
 //                 slope = d loss / d lp = -r A (0 where the clip binds) + kl (1 - exp(d))
-// Both gradients are A q_v with a few sparse terms, which one thread per target
-// writes over the dense value after a barrier.
+// Both gradients are A q_v with a few sparse terms, written over the dense value:
+// the policy's by the thread that wrote that, the distillation's one thread per
+// target, behind a barrier (loss_kernel) or in the warp that wrote it.
 //
 // Both read a row once for its statistics (maximum and sum in one pass) and, with the
 // gradient, write it once: HBM bounds them, 2 V or 4 V bytes of a BF16 token.  A row is
@@ -31,8 +32,9 @@
 //
 // loss_stream_kernel: loss and gradient of many rows.  In the kernel above reading and
 // writing take turns within a block, and at these sizes only one or two fit an SM
-// (8192 x 131072 BF16 782 us).  Here a warp of its own loads the next row while this
-// one is computed and written (656 us: 6.2 TB/s of what has to move; 16384 x 50257 policy 522 us).
+// (8192 x 131072 BF16, 64 targets, a tenth of the tokens left out: 782 us).  Here a warp
+// of its own loads the next row while this one is computed and written (638 us: 6.4 TB/s
+// of what has to move; where all count 667, the policy loss 652; its 16384 x 50257 520).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -1186,11 +1188,11 @@ __global__ void __launch_bounds__(kStreamBound, 1)
         }
       }
       // The targets' logits, from L2 where the row now is (ahead of the row they would
-      // be reads of their own from HBM: 42 us of 717 for 8191 rows of 131072 BF16 with
-      // 64 targets each; left pending behind the gradient's stores 18 us).  Each warp
-      // those whose elements it writes itself, so that no barrier is needed between the
-      // dense values and the targets' terms (with one, and the first warps taking all
-      // targets, 8192 rows with 64 each 682 us instead of 656).
+      // be reads of their own from HBM: 42 us of 717 for 8192 rows of 131072 BF16, a
+      // tenth left out, with 64 targets each; left pending behind the gradient's stores
+      // 18 us).  Each warp those whose elements it writes itself, so that no barrier is
+      // needed between the dense values and the targets' terms (with one, and the first
+      // warps taking all targets, the same rows 682 us instead of 656).
       T z_target = E::make(0.0f);
       int target = -1;
       if constexpr (KIND == kDistill) {
@@ -1368,10 +1370,26 @@ cudaError_t start_stream(const LossArgs& a, int warps, int blocks, int64_t slots
 }
 
 // Whether the call has rows enough for persistent blocks, and their launch.  By
-// bytes of a row, measured with loss and gradient (us): 100 KB (16384 x 50257 BF16)
-// two blocks per SM 515, one 580; 262 KB (8191 x 131072 BF16) one 652, two 874
-// (304 rows do not stay in L2); 524 KB (4096 x 131072 FP32) one 817, a block per row
-// with half of it on the chip 697.
+// bytes of a row (304 of the longer ones do not stay in L2), measured with loss and
+// gradient (us, distillation with 64 targets / policy):
+//                             one block per SM   two
+//   98 KB   16384 x 25001 FP32    586 / 542    526 / 552
+//   98 KB   16384 x 50257 BF16    647 / 595    537 / 519
+//   109 KB  16384 x 28001 FP32    599 / 564    596 / 614
+//   125 KB  16384 x 32000 FP32    643 / 634    697 / 706
+//   125 KB  16384 x 64000 BF16    709 / 665    685 / 711
+//   195 KB  16384 x 100003 BF16  1057 / 1035  1247 / 1256
+//   196 KB  8192 x 50257 FP32     509 / 504    618 / 622
+//                             one block per SM   a block per row, part of it on the chip
+//   312 KB  4096 x 80003 FP32     463 / 466    599 / 464
+//   351 KB  4096 x 90001 FP32     539 / 540    646 / 524
+//   378 KB  4096 x 97001 FP32     592 / 595    676 / 545
+//   390 KB  6144 x 200003 BF16    914 / 918   1119 / 918
+//   429 KB  4096 x 110003 FP32    688 / 689    727 / 615
+//   468 KB  4096 x 120001 FP32    765 / 767    801 / 682
+//   512 KB  4096 x 131072 FP32    834 / 832    798 / 697
+// (Streaming is worth more to the distillation, whose targets it brings ahead: its
+// rows cross between 468 and 512 KB, the policy's at 312.)
 constexpr int64_t kTwoRows = 112 << 10, kLongRow = 384 << 10;
 
 template <typename T, int KIND>
