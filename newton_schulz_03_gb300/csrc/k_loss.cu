@@ -1443,10 +1443,19 @@ cudaError_t start_mode(const LossArgs& a, int num_sms, cudaStream_t s) {
     // A piece each, as far as that goes.
     while (threads < (MODE == kLossOnly ? kThreads / 4 : kThreads / 2) && per > int64_t(threads) * kVecs) threads *= 2;
     // More rows than run at one time: narrower blocks, whose waits overlap with more
-    // others'.  Measured (us, a piece each / narrower; 128 threads, 256 for the last two):
-    // distillation's loss of 65536 x 4096 FP32 330 / 285, of 16384 x 16384 BF16 119 / 112
-    // (4000 vectors and more: 256 threads); gradients of 32768 x 8192 FP32 492 / 352 (policy
-    // 330 / 307), of 8388 x 32000 BF16 193 / 165 (policy 156 / 161; 8000 vectors: 321 / 324).
+    // others'.  Measured at 512 MB of BF16 logits (FP32 takes up to a tenth less, in the same
+    // order), by threads, us: loss of the distillation with 8 targets / of the policy,
+    // and their gradients from the lse:
+    //   vectors        64       128       256       64       128       256       512
+    //   300       451/296   407/284   606/497  568/312   520/281   666/471  1335/911
+    //   512       277/179   238/165   359/294  349/221   302/190   401/291   791/555
+    //   1024      182/133   154/110   180/145  250/202   219/167   236/172   428/306
+    //   1400      169/134   134/103   167/138  241/207   206/165   218/166   332/235
+    //   2048      139/116   111/90    118/97   216/195   180/160   178/156   252/173
+    //   3000      134/118   102/89    101/89   216/202   178/165   170/160   221/168
+    //   4096      118/107    93/84     92/83   201/192   171/163   165/160   187/157
+    //   6000      121/113    92/85     90/82   205/196   174/166   169/163   173/159
+    //   8000      122/116    92/86     87/82   201/197   174/168   169/166   168/161
     if (a.tokens * blocks > num_sms * int64_t(3 * kThreads / 2 / threads)) {
       const int64_t most = MODE == kLossOnly ? 2048 : 1024, wide = KIND == kDistill ? 4096 : 2048;
       if (per > int64_t(kMinThreads) * kVecs && per <= most) threads = 128;
